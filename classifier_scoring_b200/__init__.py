@@ -15,11 +15,15 @@ from typing import Optional
 
 import numpy as np
 
-__all__ = ["RmConfig", "RmError", "Scorer", "lib", "schedule", "weights_bytes", "ops",
-           "ENC_POSTLN", "DEC_PRELN", "F32", "BF16", "GELU_ERF", "GELU_TANH"]
+__all__ = ["RmConfig", "RmError", "Scorer", "KvCache", "Rope", "lib", "schedule", "weights_bytes",
+           "ops", "ENC_POSTLN", "DEC_PRELN", "F32", "BF16", "E4M3", "GELU_ERF", "GELU_TANH",
+           "ROPE_HALF", "ROPE_INTERLEAVED", "ROPE_PLAIN", "ROPE_LINEAR", "ROPE_BASE", "ROPE_PARTS"]
 
 ENC_POSTLN, DEC_PRELN = 0, 1
 F32, BF16 = 0, 1
+E4M3 = 2                    # 8-bit floats: a cache's element type (KvCache)
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_PARTS = 0, 1, 2, 3
 ROWS_RESID_F32 = 2          # res_ln rows: x fp32, y and z bf16
 ROWS_F32_IN = 3             # res_ln rows: y and x fp32, z bf16
 GELU_ERF, GELU_TANH = 0, 1
@@ -69,6 +73,46 @@ class RmConfig(ctypes.Structure):
         return c
 
 
+class _KvCacheArgs(ctypes.Structure):
+    """rm_kv_cache of include/rm_ops.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class KvCache:
+    """A paged cache of keys and values (rm_kv_cache): k and v are device pages
+    [n_pages][n_kv_heads][page_size][head_dim] of dtype BF16 or E4M3, page_stride
+    elements apart (default: packed); an E4M3 cache has a scale per head in
+    k_scale and v_scale (fp32, or both None for 1).  Keeps the buffers alive."""
+
+    def __init__(self, k, v, *, n_pages, page_size, n_kv_heads, head_dim, dtype=BF16, k_scale=None,
+                 v_scale=None, page_stride=None):
+        if page_stride is None:
+            page_stride = n_kv_heads * page_size * head_dim
+        self._args = _KvCacheArgs(_ptr(k), _ptr(v), page_stride, n_pages, page_size, n_kv_heads, head_dim,
+                                  dtype, _ptr(k_scale), _ptr(v_scale))
+        self._ref = ctypes.byref(self._args)
+        self._keep = (k, v, k_scale, v_scale)
+
+
+class _RopeArgs(ctypes.Structure):
+    """rm_rope of include/rm_ops.h."""
+    _fields_ = [("freqs", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("mscale", ctypes.c_float)]
+
+
+class Rope:
+    """How positions rotate (rm_rope): freqs is a device double[rot_dim/2] (ops.rope_freqs
+    gives the host values).  Keeps the buffer alive."""
+
+    def __init__(self, freqs, rot_dim, *, layout=ROPE_HALF, mscale=1.0):
+        self._args = _RopeArgs(_ptr(freqs), rot_dim, layout, mscale)
+        self._ref = ctypes.byref(self._args)
+        self._keep = freqs
+
+
 _lib = None
 
 
@@ -81,7 +125,8 @@ def lib() -> ctypes.CDLL:
         raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m classifier_scoring_b200.build`")
     L = ctypes.CDLL(LIB_PATH)
     P, I32, I64, F, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
-    cfgp = ctypes.POINTER(RmConfig)
+    D = ctypes.c_double
+    cfgp, cachep, ropep = (ctypes.POINTER(s) for s in (RmConfig, _KvCacheArgs, _RopeArgs))
     sig = {
         "rm_weights_bytes": (SZ, [cfgp]),
         "rm_create": (ctypes.c_int, [cfgp, P, SZ, ctypes.POINTER(P)]),
@@ -126,6 +171,14 @@ def lib() -> ctypes.CDLL:
         "rm_op_res_ln": (ctypes.c_int, [P, P, P, P, P, I32, I32, F, I32, I32, P]),
         "rm_op_head": (ctypes.c_int, [P, P, I32, P, F, I32, I32, P, P]),
         "rm_arena_plan": (ctypes.c_int, [cfgp, I32, I32, I64, P, P, P, P, I32, P]),
+        "rm_rope_freqs": (ctypes.c_int, [I32, D, I32, D, D, D, D, P]),
+        "rm_op_kv_slots": (ctypes.c_int, [P, P, I32, I32, P, I32, P, P, I32, I32, P, P, P, P, P, P, P]),
+        "rm_op_qk_norm_rope": (ctypes.c_int, [P, I64, P, I64, P, I64, I32, I32, I32, I32, P, P, F, ropep, P,
+                                              cachep, P, P]),
+        "rm_op_attn_window": (ctypes.c_int, [P, I64, P, I64, P, I64, P, I32, I32, I32, I32, I32, I32, I32, P,
+                                             I64, P]),
+        "rm_attn_decode_workspace": (SZ, [I32, I32, cachep]),
+        "rm_op_attn_decode": (ctypes.c_int, [P, I64, cachep, P, I32, P, I32, I32, I32, I32, P, I64, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -410,6 +463,56 @@ class ops:
     def head(x, offsets_dev, n_seqs, w_r, b_r, H, last_token, out, stream=None):
         _check(lib().rm_op_head(_ptr(x), _ptr(offsets_dev), n_seqs, _ptr(w_r), b_r, H,
                                 int(last_token), _ptr(out), _stream(stream)))
+
+    @staticmethod
+    def rope_freqs(rot_dim, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, trained=0.0, fast=32.0, slow=1.0):
+        """rm_rope_freqs: host float64 turning rates (radians per position)."""
+        out = np.zeros(max(1, int(rot_dim) // 2), dtype=np.float64)
+        _check(lib().rm_rope_freqs(rot_dim, base, scaling, factor, trained, fast, slow, out.ctypes.data))
+        return out
+
+    @staticmethod
+    def kv_slots(len_before, n_new, n_seqs, page_size, free_pages, n_free, used_before, block_table,
+                 table_stride, T, offsets, positions, slots, len_after, used_after, unserved, stream=None):
+        """Device buffers: int32 but for slots (int64)."""
+        _check(lib().rm_op_kv_slots(_ptr(len_before), _ptr(n_new), n_seqs, page_size, _ptr(free_pages), n_free,
+                                    _ptr(used_before), _ptr(block_table), table_stride, T, _ptr(offsets),
+                                    _ptr(positions), _ptr(slots), _ptr(len_after), _ptr(used_after),
+                                    _ptr(unserved), _stream(stream)))
+
+    @staticmethod
+    def qk_norm_rope(qkv, qkv_stride, q_out, q_stride, k_out, k_stride, T, n_q_heads, n_kv_heads, head_dim,
+                     q_gain, k_gain, eps, rope, positions, cache=None, slots=None, stream=None):
+        """rope: Rope or None; cache: KvCache or None; k_out may be None."""
+        _check(lib().rm_op_qk_norm_rope(_ptr(qkv), qkv_stride, _ptr(q_out), q_stride, _ptr(k_out), k_stride, T,
+                                        n_q_heads, n_kv_heads, head_dim, _ptr(q_gain), _ptr(k_gain), eps,
+                                        None if rope is None else rope._ref, _ptr(positions),
+                                        None if cache is None else cache._ref, _ptr(slots), _stream(stream)))
+
+    @staticmethod
+    def attn_window(q, q_stride, k, k_stride, v, v_stride, offsets_dev, n_seqs, T, n_q_heads, n_kv_heads,
+                    head_dim, window, sinks, out, out_stride, stream=None):
+        _check(lib().rm_op_attn_window(_ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride,
+                                       _ptr(offsets_dev), n_seqs, T, n_q_heads, n_kv_heads, head_dim, window,
+                                       sinks, _ptr(out), out_stride, _stream(stream)))
+
+    @staticmethod
+    def attn_decode_workspace(n_seqs, n_q_heads, cache):
+        """rm_attn_decode_workspace: bytes of device workspace for attn_decode (raises for bad sizes)."""
+        size = int(lib().rm_attn_decode_workspace(n_seqs, n_q_heads, cache._ref))
+        if size == 0:
+            raise RmError(RM_E_INVAL, "bad sizes")
+        return size
+
+    @staticmethod
+    def attn_decode(q, q_stride, cache, block_table, table_stride, length, n_seqs, n_q_heads, window, sinks,
+                    out, out_stride, workspace, workspace_bytes=None, stream=None):
+        """workspace: device buffer of attn_decode_workspace(...) bytes (its size is read from a tensor)."""
+        if workspace_bytes is None:
+            workspace_bytes = workspace.numel() * workspace.element_size()
+        _check(lib().rm_op_attn_decode(_ptr(q), q_stride, cache._ref, _ptr(block_table), table_stride,
+                                       _ptr(length), n_seqs, n_q_heads, window, sinks, _ptr(out), out_stride,
+                                       _ptr(workspace), workspace_bytes, _stream(stream)))
 
     @staticmethod
     def arena_plan(cfg: RmConfig, T, n_seqs, s_elems, max_bufs=16):

@@ -5,6 +5,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/rm.h"
+#include "../../include/rm_ops.h"
+
 namespace rmk {
 
 // ---- tcgen05 GEMM (gemm_tc.cu) ----
@@ -155,5 +158,28 @@ cudaError_t attn_context_launch(const void* S, const void* qkv, void* ctx, const
                                 const int32_t* rb_off, const int64_t* s_off, int n_seqs,
                                 int n_row_blocks, int n_heads, int head_dim, int causal,
                                 cudaStream_t st);
+
+// ---- incremental scoring (kvcache.cu, attention_window.cu, attention_decode.cu) ----
+// Arguments as in rm_ops.h, already validated.
+cudaError_t kv_slots_launch(const int32_t* len_before, const int32_t* n_new, int n, int page_size,
+                            const int32_t* free_pages, int n_free, const int32_t* used_before,
+                            int32_t* block_table, int stride, int T, int32_t* offsets,
+                            int32_t* positions, int64_t* slots, int32_t* len_after,
+                            int32_t* used_after, int32_t* unserved, cudaStream_t st);
+// rope.rot_dim 0 = no rotation; cache.k NULL = no cache write
+cudaError_t qk_norm_rope_launch(const void* qkv, int64_t qkv_stride, void* q_out, int64_t q_stride,
+                                void* k_out, int64_t k_stride, int T, int hq, int hkv, int d,
+                                const float* q_gain, const float* k_gain, float eps,
+                                const rm_rope& rope, const int32_t* positions,
+                                const rm_kv_cache& cache, const int64_t* slots, cudaStream_t st);
+cudaError_t attn_window_launch(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                               const void* v, int64_t v_stride, const int32_t* offsets, int n,
+                               int T, int hq, int hkv, int d, int window, int sinks, void* out,
+                               int64_t out_stride, cudaStream_t st);
+size_t attn_decode_workspace(int n, int hq, const rm_kv_cache& cache);
+cudaError_t attn_decode_launch(const void* q, int64_t q_stride, const rm_kv_cache& cache,
+                               const int32_t* table, int table_stride, const int32_t* length,
+                               int n, int hq, int window, int sinks, void* out, int64_t out_stride,
+                               void* workspace, cudaStream_t st);
 
 }  // namespace rmk

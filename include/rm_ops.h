@@ -240,6 +240,166 @@ int rm_op_attn_tcl(const void* qkv, void* ctx, const int32_t* offsets, const int
 int rm_op_attention_noalloc(const void* qkv, void* ctx, const int32_t* offsets, int32_t n_seqs,
                             int32_t n_heads, int32_t head_dim, int32_t causal, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Incremental scoring: a text scored as it grows, its keys and values kept in
+ * a paged cache instead of being recomputed ("Learning to summarize from human
+ * feedback" summary, method section: the reward model is a causal decoder, so
+ * earlier tokens' keys and values do not depend on later ones).  A step is
+ *   rm_op_kv_slots       where the step's new tokens go in the cache
+ *   (QKV projection)     rm_op_gemm
+ *   rm_op_qk_norm_rope   per-head norm and rotation of q and k, cache write
+ *   rm_op_attn_window    prompts: the new tokens attend to one another, or
+ *   rm_op_attn_decode    one new token per sequence attends to the cache.
+ * Unlike the steps above, these take grouped heads (n_q_heads a multiple of
+ * n_kv_heads; query head j reads key-value head j / (n_q_heads / n_kv_heads))
+ * and rows with a pitch (row_stride elements from one token to the next).
+ * Every device pointer must belong to the current CUDA device (RM_E_INVAL
+ * otherwise, host memory included).  None of them allocates or keeps anything
+ * between calls; all can be captured in a CUDA graph.
+ * ------------------------------------------------------------------------- */
+
+/* A paged cache.  Element (page p, kv head h, slot s, dim c) of the keys is
+ * k[p*page_stride + (h*page_size + s)*head_dim + c]; the values likewise.
+ * A token's slot number is p*page_size + s.  dtype RM_BF16, or RM_E4M3: 8-bit
+ * floats (4 exponent, 3 mantissa bits) standing for value * scale of the head
+ * (k_scale, v_scale: device float[n_kv_heads], > 0; both NULL = 1).  k and v
+ * are 16-byte aligned, page_stride (elements) * element size a multiple of 16
+ * and page_stride >= n_kv_heads * page_size * head_dim: pages of several
+ * layers, or keys beside values, may interleave in one allocation. */
+#define RM_E4M3 2
+typedef struct rm_kv_cache {
+  void* k;
+  void* v;
+  int64_t page_stride;
+  int32_t n_pages;
+  int32_t page_size;             /* tokens per page, 1..1024                     */
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t dtype;                 /* RM_BF16 | RM_E4M3                            */
+  const float* k_scale;
+  const float* v_scale;
+} rm_kv_cache;
+
+/* How positions rotate: pair i of the first rot_dim dims of a head turns by
+ * position * freqs[i] radians (freqs: device double[rot_dim/2], see
+ * rm_rope_freqs); the other dims stay.  layout RM_ROPE_HALF pairs dims i and
+ * i + rot_dim/2, RM_ROPE_INTERLEAVED dims 2i and 2i+1.  The rotated pair is
+ * multiplied by mscale (1 for none). */
+#define RM_ROPE_HALF        0
+#define RM_ROPE_INTERLEAVED 1
+typedef struct rm_rope {
+  const double* freqs;
+  int32_t rot_dim;               /* even, 0..head_dim; 0 = no rotation           */
+  int32_t layout;
+  float mscale;
+} rm_rope;
+
+/* Host only: the turning rates f_i = base^(-2i/rot_dim), i < rot_dim/2, and
+ * their changes for contexts longer than a model was trained on:
+ *   RM_ROPE_PLAIN    f_i
+ *   RM_ROPE_LINEAR   f_i / factor (positions interpolated)
+ *   RM_ROPE_BASE     base * factor^(rot_dim/(rot_dim-2)) in place of base, so
+ *                    that the slowest pair is stretched by factor and the
+ *                    fastest stays (rot_dim > 2)
+ *   RM_ROPE_PARTS    per pair, by how often it turns over trained tokens (Peng
+ *                    et al., "YaRN: Efficient Context Window Extension of
+ *                    Large Language Models", section 3.2): pairs that turn
+ *                    more than fast times keep f_i, those that turn less than
+ *                    slow times take f_i / factor, between them linearly in
+ *                    the number of turns.
+ * freqs: host double[rot_dim/2].  factor >= 1; trained >= 1 and fast > slow > 0
+ * are read by RM_ROPE_PARTS only.  RM_E_INVAL for anything else. */
+#define RM_ROPE_PLAIN  0
+#define RM_ROPE_LINEAR 1
+#define RM_ROPE_BASE   2
+#define RM_ROPE_PARTS  3
+int rm_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, double trained,
+                  double fast, double slow, double* freqs);
+
+/* Block tables and slot maps of a step, built on the device from the request
+ * lengths.  Sequence i holds len_before[i] tokens and gets n_new[i] more (0 or
+ * more).  Its tokens need ceil(len / page_size) pages; the ones it lacks come
+ * from free_pages[*used_before ..] in request order and are written to its
+ * row of block_table ([n_seqs][table_stride]).  Written:
+ *   offsets[n_seqs+1]   packed offsets of the new tokens
+ *   positions[T], slots[T]  position in the sequence and cache slot of each
+ *                       new token; entries behind the last token up to T (a
+ *                       padded batch) get position 0 and slot -1
+ *   len_after[n_seqs]   len_before + n_new
+ *   used_after[1]       *used_before plus the pages taken
+ *   unserved[1]         how many sequences did not fit (0 normally): the
+ *                       first whose pages exceed n_free, whose new tokens
+ *                       exceed T, whose row exceeds table_stride pages or
+ *                       whose length is negative, and every one behind it.
+ *                       These get no tokens and no pages, and len_after =
+ *                       len_before; a later call may serve them.
+ * len_after may be len_before and used_after may be used_before (a captured
+ * step that advances itself); no other buffers may overlap.  Page numbers of
+ * free_pages and of block_table are copied, not checked.  n_seqs <= 16384. */
+int rm_op_kv_slots(const int32_t* len_before, const int32_t* n_new, int32_t n_seqs,
+                   int32_t page_size, const int32_t* free_pages, int32_t n_free,
+                   const int32_t* used_before, int32_t* block_table, int32_t table_stride,
+                   int32_t T, int32_t* offsets, int32_t* positions, int64_t* slots,
+                   int32_t* len_after, int32_t* used_after, int32_t* unserved, void* stream);
+
+/* Norm and rotation of a projection's queries and keys, and the cache write,
+ * in one pass.  Row t of qkv holds the token's query heads, then its key
+ * heads, then its value heads, head_dim elements each (bf16).  Per head:
+ *   y = x / sqrt(mean(x^2) + eps) * gain      (q_gain, k_gain: fp32 [head_dim];
+ *                                              both NULL = no norm)
+ *   z = y with its first rot_dim dims rotated by positions[t] (rope NULL: z = y)
+ * in fp32, angles reduced in 64 bits (exact to fp32 rounding for any int32
+ * position), rounded once.  Written: q_out (row t's query heads), k_out (its
+ * key heads; NULL = not written), and, when cache != NULL, the key and value
+ * heads to slots[t] of the cache (bf16, or x / scale rounded to the nearest
+ * 8-bit value, +-448 at most, NaN kept).  A token whose slot is negative or
+ * beyond the cache's last page is not written to the cache.  Two tokens must
+ * not share a slot.  q_out and k_out may be the q and k columns of qkv itself
+ * (in place); no other overlap.
+ * head_dim a multiple of 8, 8..256; qkv, q_out, k_out 16-byte aligned with
+ * strides that are multiples of 8 elements; T >= 0. */
+int rm_op_qk_norm_rope(const void* qkv, int64_t qkv_stride, void* q_out, int64_t q_stride,
+                       void* k_out, int64_t k_stride, int32_t T, int32_t n_q_heads,
+                       int32_t n_kv_heads, int32_t head_dim, const float* q_gain,
+                       const float* k_gain, float eps, const rm_rope* rope,
+                       const int32_t* positions, const rm_kv_cache* cache, const int64_t* slots,
+                       void* stream);
+
+/* Causal attention of packed sequences with a sliding window and sinks: token
+ * t of a sequence sees its key j <= t when j > t - window or j < sinks (window
+ * 0: every j <= t).  out = softmax(q k^T / sqrt(head_dim)) v over the seen
+ * keys, fp32 softmax, P rounded to bf16 before the product with V (its rows'
+ * sums are taken before that rounding).  q, out: [T][n_q_heads*head_dim], k,
+ * v: [T][n_kv_heads*head_dim], bf16, each with its row stride; offsets: DEVICE
+ * int32[n_seqs+1], offsets[0] = 0, non-decreasing (empty sequences allowed),
+ * offsets[n_seqs] <= T; rows behind it are neither read nor written.  Values
+ * and keys that a row does not see do not reach it, infinities and NaN among
+ * them.  head_dim 64 or 128; pointers 16-byte aligned, strides multiples of 8
+ * elements; n_q_heads / n_kv_heads <= 128. */
+int rm_op_attn_window(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                      const void* v, int64_t v_stride, const int32_t* offsets, int32_t n_seqs,
+                      int32_t T, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                      int32_t window, int32_t sinks, void* out, int64_t out_stride, void* stream);
+
+/* The same attention for one new token per sequence over the paged cache: row
+ * i of q is the query of the last of length[i] tokens of sequence i, whose
+ * keys and values lie in pages block_table[i*table_stride ..] in order (the
+ * new token's own among them).  length[i] <= 0 gives a row of zeros; lengths
+ * beyond table_stride * page_size are cut to it.  A page number outside
+ * 0..n_pages-1 drops its page's tokens.  The work is split over the lengths
+ * and joined in a fixed order (the same call gives the same bits); partial
+ * results go to workspace: device memory of rm_attn_decode_workspace bytes,
+ * 16-byte aligned, overwritten, which no other call may use at the same time
+ * (calls captured in graphs that may overlap need workspaces of their own).
+ * Pages that a window hides are not read.  cache->head_dim 64 or 128. */
+int rm_op_attn_decode(const void* q, int64_t q_stride, const rm_kv_cache* cache,
+                      const int32_t* block_table, int32_t table_stride, const int32_t* length,
+                      int32_t n_seqs, int32_t n_q_heads, int32_t window, int32_t sinks, void* out,
+                      int64_t out_stride, void* workspace, size_t workspace_bytes, void* stream);
+/* Host only: the workspace bytes of rm_op_attn_decode for up to n_seqs
+ * sequences, whatever their lengths (0 for bad sizes). */
+size_t rm_attn_decode_workspace(int32_t n_seqs, int32_t n_q_heads, const rm_kv_cache* cache);
+
 /* Residual + LayerNorm over rows of length H (the LayerNorm batch reduction of
  * the TurboTransformers abstract), fp32 math:
  *   mode 0 (post-LN): x = LN(y + x)              (z unused, may be NULL)
