@@ -12,7 +12,7 @@ namespace {
 
 // Every pointer is memory of the current device: a host pointer, or one of
 // another device, would fault in the kernel.  NULL entries are skipped.
-int check_on_device(std::initializer_list<const void*> ptrs) {
+int check_on_device(std::initializer_list<const void*> ptrs, int* num_sms = nullptr) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) {
@@ -29,6 +29,10 @@ int check_on_device(std::initializer_list<const void*> ptrs) {
     }
     if ((a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) || a.device != dev)
       return set_error(RM_E_INVAL, "pointer %p is not memory of the current device %d", p, dev);
+  }
+  if (num_sms != nullptr) {
+    e = cudaDeviceGetAttribute(num_sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return set_error(RM_E_CUDA, "%s", cudaGetErrorString(e));
   }
   return RM_OK;
 }
@@ -226,10 +230,11 @@ int rm_op_attn_decode(const void* q, int64_t q_stride, const rm_kv_cache* cache,
     return set_error(RM_E_INVAL, "q, out and workspace must be 16-byte aligned");
   if (workspace_bytes < attn_decode_workspace(n_seqs, n_q_heads, *cache))
     return set_error(RM_E_RANGE, "workspace too small (rm_attn_decode_workspace)");
+  int sms = 0;
   RM_CHECK(check_on_device({q, cache->k, cache->v, cache->k_scale, cache->v_scale, block_table,
-                            length, out, workspace}));
+                            length, out, workspace}, &sms));
   RM_LAUNCH(attn_decode_launch(q, q_stride, *cache, block_table, table_stride, length, n_seqs,
-                               n_q_heads, window, sinks, out, out_stride, workspace,
+                               n_q_heads, window, sinks, out, out_stride, workspace, sms,
                                static_cast<cudaStream_t>(stream)));
   return RM_OK;
 }

@@ -180,6 +180,6 @@ size_t attn_decode_workspace(int n, int hq, const rm_kv_cache& cache);
 cudaError_t attn_decode_launch(const void* q, int64_t q_stride, const rm_kv_cache& cache,
                                const int32_t* table, int table_stride, const int32_t* length,
                                int n, int hq, int window, int sinks, void* out, int64_t out_stride,
-                               void* workspace, cudaStream_t st);
+                               void* workspace, int num_sms, cudaStream_t st);
 
 }  // namespace rmk
