@@ -48,6 +48,10 @@ cudaError_t gemm_launch(const CUtensorMap& a, const CUtensorMap& b, const CUtens
 // zero fill outside.  Returns false (message in *why) if the driver refuses it.
 bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                     uint32_t box_rows, const char** why);
+// 3-D bf16 tensor [rows][heads][dim] whose rows lie row_stride elements apart,
+// box {64 dims, box_heads, box_rows}, 128-byte swizzle, zero fill outside.
+bool make_tmap_heads(CUtensorMap* map, const void* base, uint64_t rows, uint64_t heads, uint64_t dim,
+                     uint64_t row_stride, uint32_t box_heads, uint32_t box_rows, const char** why);
 // 2-D row-major [rows][cols] output of the GEMM (bf16, or fp32 when f32), box
 // {32 cols, 32 rows}, 64-byte (bf16) or 128-byte (fp32) swizzle: the layout of
 // the GEMM epilogue's staging boxes.  Stores outside the tensor are clipped.
@@ -175,7 +179,7 @@ cudaError_t qk_norm_rope_launch(const void* qkv, int64_t qkv_stride, void* q_out
 cudaError_t attn_window_launch(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                const void* v, int64_t v_stride, const int32_t* offsets, int n,
                                int T, int hq, int hkv, int d, int window, int sinks, void* out,
-                               int64_t out_stride, cudaStream_t st);
+                               int64_t out_stride, int num_sms, cudaStream_t st);
 size_t attn_decode_workspace(int n, int hq, const rm_kv_cache& cache);
 cudaError_t attn_decode_launch(const void* q, int64_t q_stride, const rm_kv_cache& cache,
                                const int32_t* table, int table_stride, const int32_t* length,

@@ -1,8 +1,9 @@
 // Slot maps of a paged cache, and the norm, rotation and cache write of a
 // step's queries and keys.
 #include <cooperative_groups.h>
+#include <cuda_fp8.h>
 
-#include "attend_row.cuh"
+#include "common.cuh"
 #include "kernels.h"
 
 namespace rmk {
