@@ -173,12 +173,13 @@ int rm_op_qk_norm_rope(const void* qkv, int64_t qkv_stride, void* q_out, int64_t
       return set_error(RM_E_INVAL, "the cache has other heads");
   }
   if (T == 0) return RM_OK;
+  int sms = 0;
   RM_CHECK(check_on_device({qkv, q_out, k_out, q_gain, k_gain, r.rot_dim > 0 ? r.freqs : nullptr,
                             r.rot_dim > 0 ? positions : nullptr, c.k, c.v, c.k_scale, c.v_scale,
-                            cache != nullptr ? slots : nullptr}));
+                            cache != nullptr ? slots : nullptr}, &sms));
   RM_LAUNCH(qk_norm_rope_launch(qkv, qkv_stride, q_out, q_stride, k_out, k_stride, T, n_q_heads,
                                 n_kv_heads, head_dim, q_gain, k_gain, eps, r, positions, c, slots,
-                                static_cast<cudaStream_t>(stream)));
+                                sms, static_cast<cudaStream_t>(stream)));
   return RM_OK;
 }
 

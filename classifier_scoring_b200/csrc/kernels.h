@@ -175,7 +175,8 @@ cudaError_t qk_norm_rope_launch(const void* qkv, int64_t qkv_stride, void* q_out
                                 void* k_out, int64_t k_stride, int T, int hq, int hkv, int d,
                                 const float* q_gain, const float* k_gain, float eps,
                                 const rm_rope& rope, const int32_t* positions,
-                                const rm_kv_cache& cache, const int64_t* slots, cudaStream_t st);
+                                const rm_kv_cache& cache, const int64_t* slots, int num_sms,
+                                cudaStream_t st);
 cudaError_t attn_window_launch(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                const void* v, int64_t v_stride, const int32_t* offsets, int n,
                                int T, int hq, int hkv, int d, int window, int sinks, void* out,
