@@ -91,8 +91,8 @@ class KvCache:
                  v_scale=None, page_stride=None):
         if page_stride is None:
             page_stride = n_kv_heads * page_size * head_dim
-        self._args = _KvCacheArgs(_ptr(k), _ptr(v), page_stride, n_pages, page_size, n_kv_heads, head_dim,
-                                  dtype, _ptr(k_scale), _ptr(v_scale))
+        kp, vp, ks, vs = _on_one_device(k, v, k_scale, v_scale)
+        self._args = _KvCacheArgs(kp, vp, page_stride, n_pages, page_size, n_kv_heads, head_dim, dtype, ks, vs)
         self._ref = ctypes.byref(self._args)
         self._keep = (k, v, k_scale, v_scale)
 
@@ -202,6 +202,23 @@ def _ptr(x) -> Optional[int]:
     if isinstance(x, np.ndarray):
         return x.ctypes.data
     return int(x)
+
+
+def _on_one_device(*xs) -> list:
+    """The addresses of device buffers; tensors among them must lie on one CUDA device."""
+    found, dev = [], None
+    for x in xs:
+        if x is None or type(x) is int:
+            found.append(x)
+            continue
+        if hasattr(x, "get_device"):
+            d = x.get_device()
+            if dev is None:
+                dev = d
+            if d != dev or d < 0:
+                raise RmError(RM_E_INVAL, "every buffer must be memory of the same CUDA device")
+        found.append(_ptr(x))
+    return found
 
 
 def _stream(s) -> Optional[int]:
@@ -475,26 +492,29 @@ class ops:
     def kv_slots(len_before, n_new, n_seqs, page_size, free_pages, n_free, used_before, block_table,
                  table_stride, T, offsets, positions, slots, len_after, used_after, unserved, stream=None):
         """Device buffers: int32 but for slots (int64)."""
-        _check(lib().rm_op_kv_slots(_ptr(len_before), _ptr(n_new), n_seqs, page_size, _ptr(free_pages), n_free,
-                                    _ptr(used_before), _ptr(block_table), table_stride, T, _ptr(offsets),
-                                    _ptr(positions), _ptr(slots), _ptr(len_after), _ptr(used_after),
-                                    _ptr(unserved), _stream(stream)))
+        b, m, f, u, tab, off, pos, sl, la, ua, un = _on_one_device(
+            len_before, n_new, free_pages, used_before, block_table, offsets, positions, slots, len_after,
+            used_after, unserved)
+        _check(lib().rm_op_kv_slots(b, m, n_seqs, page_size, f, n_free, u, tab, table_stride, T, off, pos, sl, la,
+                                    ua, un, _stream(stream)))
 
     @staticmethod
     def qk_norm_rope(qkv, qkv_stride, q_out, q_stride, k_out, k_stride, T, n_q_heads, n_kv_heads, head_dim,
                      q_gain, k_gain, eps, rope, positions, cache=None, slots=None, stream=None):
         """rope: Rope or None; cache: KvCache or None; k_out may be None."""
-        _check(lib().rm_op_qk_norm_rope(_ptr(qkv), qkv_stride, _ptr(q_out), q_stride, _ptr(k_out), k_stride, T,
-                                        n_q_heads, n_kv_heads, head_dim, _ptr(q_gain), _ptr(k_gain), eps,
-                                        None if rope is None else rope._ref, _ptr(positions),
-                                        None if cache is None else cache._ref, _ptr(slots), _stream(stream)))
+        x, qo, ko, gq, gk, pos, sl, _, _ = _on_one_device(
+            qkv, q_out, k_out, q_gain, k_gain, positions, slots, None if rope is None else rope._keep,
+            None if cache is None else cache._keep[0])
+        _check(lib().rm_op_qk_norm_rope(x, qkv_stride, qo, q_stride, ko, k_stride, T, n_q_heads, n_kv_heads,
+                                        head_dim, gq, gk, eps, None if rope is None else rope._ref, pos,
+                                        None if cache is None else cache._ref, sl, _stream(stream)))
 
     @staticmethod
     def attn_window(q, q_stride, k, k_stride, v, v_stride, offsets_dev, n_seqs, T, n_q_heads, n_kv_heads,
                     head_dim, window, sinks, out, out_stride, stream=None):
-        _check(lib().rm_op_attn_window(_ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride,
-                                       _ptr(offsets_dev), n_seqs, T, n_q_heads, n_kv_heads, head_dim, window,
-                                       sinks, _ptr(out), out_stride, _stream(stream)))
+        q, k, v, off, o = _on_one_device(q, k, v, offsets_dev, out)
+        _check(lib().rm_op_attn_window(q, q_stride, k, k_stride, v, v_stride, off, n_seqs, T, n_q_heads,
+                                       n_kv_heads, head_dim, window, sinks, o, out_stride, _stream(stream)))
 
     @staticmethod
     def attn_decode_workspace(n_seqs, n_q_heads, cache):
@@ -510,9 +530,9 @@ class ops:
         """workspace: device buffer of attn_decode_workspace(...) bytes (its size is read from a tensor)."""
         if workspace_bytes is None:
             workspace_bytes = workspace.numel() * workspace.element_size()
-        _check(lib().rm_op_attn_decode(_ptr(q), q_stride, cache._ref, _ptr(block_table), table_stride,
-                                       _ptr(length), n_seqs, n_q_heads, window, sinks, _ptr(out), out_stride,
-                                       _ptr(workspace), workspace_bytes, _stream(stream)))
+        q, tab, ln, o, ws, _ = _on_one_device(q, block_table, length, out, workspace, cache._keep[0])
+        _check(lib().rm_op_attn_decode(q, q_stride, cache._ref, tab, table_stride, ln, n_seqs, n_q_heads, window,
+                                       sinks, o, out_stride, ws, workspace_bytes, _stream(stream)))
 
     @staticmethod
     def arena_plan(cfg: RmConfig, T, n_seqs, s_elems, max_bufs=16):

@@ -4,6 +4,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -12,23 +13,37 @@ namespace rmk {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Slot maps.  One cluster of CTAs: every CTA scans the n requests for itself
-// (n is small beside the tokens; a scan costs less than handing its result
-// on), the cluster's barrier separates the reads of len_before and
-// used_before from the writes of len_after and used_after, which may be the
-// same memory, and the tokens and new pages are shared out over all threads.
+// Slot maps.  Bound by latency: a few dependent reads, a scan and the writes.
+// Every CTA scans the n requests for itself (n is small beside the tokens, and
+// a scan costs less than handing its result on through memory), then the
+// tokens and new pages are shared out over all threads.  len_after and
+// used_after may be len_before and used_before: then all CTAs form one cluster
+// whose barrier separates the reads from the writes.
 // ---------------------------------------------------------------------------
-constexpr int kSlotThreads = 1024;
 constexpr int kSlotRun = 8;
 
-__global__ void __launch_bounds__(kSlotThreads, 1)
-    kv_slots_kernel(const int32_t* len_before, const int32_t* n_new, int n, int P,
+// x / P = x * mul >> shift for 0 <= x < 2^31, P = 1..1024 (2^shift = 2^31 * the
+// power of two from P on: the multiplier fits 32 bits and exceeds 2^shift / P
+// by less than 1, so the quotient is too large by less than 1 / P)
+struct PageDiv {
+  uint32_t mul;
+  int shift, P;
+  __device__ __forceinline__ int floor(int x) const {
+    return static_cast<int>((static_cast<unsigned long long>(static_cast<uint32_t>(x)) * mul) >> shift);
+  }
+  __device__ __forceinline__ int ceil(int x) const {
+    const int q = floor(x);
+    return q + (x - q * P > 0);
+  }
+};
+
+__global__ void __launch_bounds__(1024, 1)
+    kv_slots_kernel(const int32_t* len_before, const int32_t* n_new, int n, PageDiv div,
                     const int32_t* __restrict__ free_pages, int n_free, const int32_t* used_before,
                     int32_t* block_table, int stride, int T, int32_t* __restrict__ offsets,
                     int32_t* __restrict__ positions, int64_t* __restrict__ slots,
-                    int32_t* len_after, int32_t* used_after, int32_t* __restrict__ unserved, bool wide) {
-  namespace cg = cooperative_groups;
-  cg::cluster_group cluster = cg::this_cluster();
+                    int32_t* len_after, int32_t* used_after, int32_t* __restrict__ unserved,
+                    bool wide, bool cluster) {
   extern __shared__ int32_t sh[];
   int32_t* off = sh;               // [n+1] first new token of request i
   int32_t* pg = off + n + 1;       // [n+1] first new page of request i
@@ -36,27 +51,31 @@ __global__ void __launch_bounds__(kSlotThreads, 1)
   __shared__ long long wsum_t[32], wsum_p[32];
   __shared__ int first_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int threads = blockDim.x, P = div.P;
   if (tid == 0) first_bad = n;
   const int used = *used_before;
 
-  // each thread sums a stretch of requests, then the stretches are scanned
-  const int per = (n + kSlotThreads - 1) / kSlotThreads;
+  // each thread sums a stretch of requests, then the stretches are scanned.
+  // A request that can never be served counts as one token and page too many.
+  const int per = (n + threads - 1) / threads;
   const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
+  auto never = [&](int b, int m) { return b < 0 || m < 0 || m > 0x7fffffff - b; };
   long long st = 0, sp = 0;
   for (int i = i0; i < i1; ++i) {
-    const int b = len_before[i];
-    const long long e = static_cast<long long>(b) + n_new[i];
+    const int b = len_before[i], m = n_new[i];
     before[i] = b;
-    st += n_new[i];
-    sp += (e + P - 1) / P - (static_cast<long long>(b) + P - 1) / P;
+    off[i] = m;
+    if (never(b, m)) continue;
+    st += m;
+    sp += div.ceil(b + m) - div.ceil(b);
   }
   long long ct = st, cp = sp;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long a = __shfl_up_sync(0xffffffffu, ct, o), b = __shfl_up_sync(0xffffffffu, cp, o);
+    const long long x = __shfl_up_sync(0xffffffffu, ct, o), y = __shfl_up_sync(0xffffffffu, cp, o);
     if (lane >= o) {
-      ct += a;
-      cp += b;
+      ct += x;
+      cp += y;
     }
   }
   if (lane == 31) {
@@ -65,21 +84,27 @@ __global__ void __launch_bounds__(kSlotThreads, 1)
   }
   __syncthreads();
   long long bt = ct - st, bp = cp - sp;
-  for (int w = 0; w < warp; ++w) {
-    bt += wsum_t[w];
-    bp += wsum_p[w];
+  {
+    long long x = lane < warp ? wsum_t[lane] : 0, y = lane < warp ? wsum_p[lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      x += __shfl_xor_sync(0xffffffffu, x, o);
+      y += __shfl_xor_sync(0xffffffffu, y, o);
+    }
+    bt += x;
+    bp += y;
   }
   // the first request that does not fit ends the served ones; the sums of
-  // later ones may be anything and are not used
+  // later ones are not used
   for (int i = i0; i < i1; ++i) {
-    const long long b = before[i], nn = n_new[i];
-    const long long have = (b + P - 1) / P, need = (b + nn + P - 1) / P;
+    const int b = before[i], m = off[i];
+    const bool no = never(b, m);
+    const int need = no ? 0 : div.ceil(b + m), have = no ? 0 : div.ceil(b);
     off[i] = static_cast<int32_t>(bt);
     pg[i] = static_cast<int32_t>(bp);
-    bt += nn;
+    bt += no ? 0 : m;
     bp += need - have;
-    if (b < 0 || nn < 0 || need > stride || bt > T || used < 0 ||
-        bp > static_cast<long long>(n_free) - used)
+    if (no || need > stride || bt > T || used < 0 || bp > static_cast<long long>(n_free) - used)
       atomicMin(&first_bad, i);
     if (i + 1 == n) {
       off[n] = static_cast<int32_t>(bt);
@@ -89,10 +114,11 @@ __global__ void __launch_bounds__(kSlotThreads, 1)
   __syncthreads();
   const int m = first_bad;
   const int tokens = off[m], pages = pg[m];
-  cluster.sync();                  // every CTA has read what the writes below may replace
+  if (cluster)                     // every CTA has read what the writes below may replace
+    cooperative_groups::this_cluster().sync();
 
-  const int at = static_cast<int>(cluster.block_rank()) * kSlotThreads + tid;
-  const int all = static_cast<int>(cluster.num_blocks()) * kSlotThreads;
+  const int at = static_cast<int>(blockIdx.x) * threads + tid;
+  const int all = static_cast<int>(gridDim.x) * threads;
   for (int i = at; i <= n; i += all) {
     offsets[i] = i < m ? off[i] : tokens;
     if (i < n) len_after[i] = before[i] + (i < m ? off[i + 1] - off[i] : 0);
@@ -103,8 +129,7 @@ __global__ void __launch_bounds__(kSlotThreads, 1)
   }
   for (int g = at; g < pages; g += all) {
     const int i = upper_index(pg, m, g);
-    const int have = (before[i] + P - 1) / P;
-    block_table[static_cast<int64_t>(i) * stride + have + (g - pg[i])] = free_pages[used + g];
+    block_table[static_cast<int64_t>(i) * stride + div.ceil(before[i]) + (g - pg[i])] = free_pages[used + g];
   }
   // kSlotRun consecutive tokens a thread: one search for their request, one
   // page lookup per page, wide stores
@@ -125,7 +150,7 @@ __global__ void __launch_bounds__(kSlotThreads, 1)
         do ++i; while (off[i + 1] <= t + k);
         p = before[i] + static_cast<int>(t + k - off[i]);
         left = static_cast<int>(off[i + 1] - (t + k));
-        b = p / P;
+        b = div.floor(p);
         rem = p - b * P;
         look = true;
       } else if (rem == P) {
@@ -134,7 +159,7 @@ __global__ void __launch_bounds__(kSlotThreads, 1)
         look = true;
       }
       if (look) {
-        const int have = (before[i] + P - 1) / P;
+        const int have = div.ceil(before[i]);
         page = b < have ? block_table[static_cast<int64_t>(i) * stride + b]
                         : free_pages[used + pg[i] + b - have];
       }
@@ -186,7 +211,7 @@ struct RopeArgs {
   int64_t k_stride;
   int T, hq, hkv, d, heads;                   // heads: those the call has to look at
   const float *q_gain, *k_gain;
-  float eps;
+  float eps, inv_d;
   const double* freqs;
   int rot, interleaved;
   float mscale;
@@ -223,19 +248,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(const Rop
   const int c = lane % LP, sub = lane / LP;   // this lane's dims 8c..8c+7 of its head
   const bool live = 8 * c < a.d;
   const int h0 = part * a.per_part, h1 = min(a.heads, h0 + a.per_part);
-  const bf16* src = a.qkv + t * a.qkv_stride + 8 * c;
-  uint4 raw[kRopeBatch];
-  auto load = [&](int h) {
-#pragma unroll
-    for (int b = 0; b < kRopeBatch; ++b) {
-      const int hh = h + b * kPer + sub;
-      if (live && hh < h1) raw[b] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(hh) * a.d);
-    }
-  };
-  load(h0);
-
   const int half = a.rot / 2;
-  float cs[8], sn[8];                         // of the lane's dims: y = x cs + partner sn
+  uint64_t cs[4], sn[4];                      // of the lane's dims: y = x cs + partner sn
   if (half > 0) {
     const double pos = a.positions[t];
     for (int i = lane; i < half; i += 32) {
@@ -247,23 +261,24 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(const Rop
       trig[warp][1][i] = s * a.mscale;
     }
     __syncwarp();
+    float f[16];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const int dim = 8 * c + e;
-      cs[e] = 1.f;
-      sn[e] = 0.f;
+      f[e] = 1.f;
+      f[8 + e] = 0.f;
       if (dim < a.rot) {
         const bool second = a.interleaved ? (e & 1) : dim >= half;
         const int i = a.interleaved ? dim >> 1 : (second ? dim - half : dim);
-        cs[e] = trig[warp][0][i];
-        sn[e] = second ? trig[warp][1][i] : -trig[warp][1][i];
+        f[e] = trig[warp][0][i];
+        f[8 + e] = second ? trig[warp][1][i] : -trig[warp][1][i];
       }
     }
-  }
-  float gq[8], gk[8];
-  if (a.q_gain != nullptr && live) {
-    load_f32x8(a.q_gain + 8 * c, gq);
-    load_f32x8(a.k_gain + 8 * c, gk);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      cs[e] = f32x2_pack(f[2 * e], f[2 * e + 1]);
+      sn[e] = f32x2_pack(f[8 + 2 * e], f[8 + 2 * e + 1]);
+    }
   }
   int64_t cache_row = -1;
   if (a.kc != nullptr) {
@@ -278,77 +293,120 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(const Rop
   const float* head = swap[warp] + sub * LP * 8;
   const bool whole = half % 8 == 0;           // chunks pair with chunks
   const int partner = 8 * c < half ? 8 * c + half : 8 * c - half;
+  const bool turns = 8 * c < a.rot;
 
-  for (int h = h0; h < h1; h += kRopeBatch * kPer) {
-    uint4 now[kRopeBatch];
+  // heads [ha, hb) of one kind; head h of the row is head h - first of its
+  // kind, written to out (row of this token, or null) and to the cache
+  auto section = [&](auto kind, int ha, int hb, int first, const float* gain_at, bf16* out, E* cache,
+                     const float* scale) {
+    constexpr bool kValue = decltype(kind)::value;
+    if (ha >= hb) return;
+    const bool norm = !kValue && gain_at != nullptr;
+    uint64_t gain[4];
+    if (norm && live) {
+      const float4 g0 = reinterpret_cast<const float4*>(gain_at + 8 * c)[0];
+      const float4 g1 = reinterpret_cast<const float4*>(gain_at + 8 * c)[1];
+      gain[0] = f32x2_pack(g0.x, g0.y);
+      gain[1] = f32x2_pack(g0.z, g0.w);
+      gain[2] = f32x2_pack(g1.x, g1.y);
+      gain[3] = f32x2_pack(g1.z, g1.w);
+    }
+    const bf16* src = a.qkv + t * a.qkv_stride + 8 * c + static_cast<int64_t>(ha + sub) * a.d;
+    const int step = kPer * a.d, cache_head = a.page_size * a.d;
+    int own = ha + sub - first;               // this lane's head among its kind
+    bf16* dst = out == nullptr ? nullptr : out + static_cast<int64_t>(own) * a.d + 8 * c;
+    E* cdst = cache == nullptr ? nullptr : cache + cache_row + static_cast<int64_t>(own) * cache_head + 8 * c;
+    for (int h = ha + sub; h - sub < hb; h += kRopeBatch * kPer) {
+      uint4 raw[kRopeBatch];
 #pragma unroll
-    for (int b = 0; b < kRopeBatch; ++b) now[b] = raw[b];
-    if (h + kRopeBatch * kPer < h1) load(h + kRopeBatch * kPer);
-#pragma unroll
-    for (int b = 0; b < kRopeBatch; ++b) {
-      if (h + b * kPer >= h1) break;
-      const int hh = h + b * kPer + sub;
-      const bool on = live && hh < h1;
-      const bool is_v = hh >= a.hq + a.hkv, is_q = hh < a.hq;
-      float x[8] = {};
-      if (on) {
-        const uint4 v = now[b];
-        x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x); x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
-        x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z); x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
+      for (int b = 0; b < kRopeBatch; ++b) {
+        raw[b] = make_uint4(0u, 0u, 0u, 0u);
+        if (live && h + b * kPer < hb) raw[b] = *reinterpret_cast<const uint4*>(src + b * step);
       }
-      if (a.q_gain != nullptr) {
-        float ss = 0.f;
+      src += kRopeBatch * step;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-        ss = group_sum<LP>(ss);
-        if (!is_v) {
-          const float inv = 1.f / sqrtf(ss / static_cast<float>(a.d) + a.eps);
+      for (int b = 0; b < kRopeBatch; ++b) {
+        if (h - sub + b * kPer >= hb) break;
+        uint64_t x[4] = {f32x2_pack(bf16_lo(raw[b].x), bf16_hi(raw[b].x)), f32x2_pack(bf16_lo(raw[b].y), bf16_hi(raw[b].y)),
+                         f32x2_pack(bf16_lo(raw[b].z), bf16_hi(raw[b].z)), f32x2_pack(bf16_lo(raw[b].w), bf16_hi(raw[b].w))};
+        if (norm) {
+          uint64_t ss2 = f32x2_mul(x[0], x[0]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= inv * (is_q ? gq[e] : gk[e]);
+          for (int e = 1; e < 4; ++e) ss2 = f32x2_fma(x[e], x[e], ss2);
+          float s0, s1;
+          f32x2_unpack(ss2, s0, s1);
+          const float ss = group_sum<LP>(s0 + s1);
+          const uint64_t inv = f32x2_splat(rsqrtf(fmaf(ss, a.inv_d, a.eps)));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = f32x2_mul(f32x2_mul(x[e], inv), gain[e]);
         }
-      }
-      if (half > 0) {
-        float y[8];
-        if (a.interleaved) {
+        if (!kValue && half > 0) {
+          uint64_t y[4];
+          if (a.interleaved) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
-        } else {
-          __syncwarp();
-          *reinterpret_cast<float4*>(mine) = make_float4(x[0], x[1], x[2], x[3]);
-          *reinterpret_cast<float4*>(mine + 4) = make_float4(x[4], x[5], x[6], x[7]);
-          __syncwarp();
-          if (8 * c < a.rot) {
-            if (whole) {
-              load_f32x8(head + partner, y);
-            } else {
+            for (int e = 0; e < 4; ++e) {
+              float lo, hi;
+              f32x2_unpack(x[e], lo, hi);
+              y[e] = f32x2_pack(hi, lo);
+            }
+          } else {
+            __syncwarp();
+            reinterpret_cast<ulonglong2*>(mine)[0] = make_ulonglong2(x[0], x[1]);
+            reinterpret_cast<ulonglong2*>(mine)[1] = make_ulonglong2(x[2], x[3]);
+            __syncwarp();
+            if (turns) {
+              if (whole) {
+                const ulonglong2 y0 = reinterpret_cast<const ulonglong2*>(head + partner)[0];
+                const ulonglong2 y1 = reinterpret_cast<const ulonglong2*>(head + partner)[1];
+                y[0] = y0.x; y[1] = y0.y; y[2] = y1.x; y[3] = y1.y;
+              } else {
+                float f[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int dim = 8 * c + e;
-                y[e] = dim < a.rot ? head[dim < half ? dim + half : dim - half] : 0.f;
+                for (int e = 0; e < 8; ++e) {
+                  const int dim = 8 * c + e;
+                  f[e] = dim < a.rot ? head[dim < half ? dim + half : dim - half] : 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = f32x2_pack(f[2 * e], f[2 * e + 1]);
               }
             }
           }
-        }
-        if (!is_v && 8 * c < a.rot) {
+          if (turns) {
+            if (8 * c + 8 <= a.rot) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], cs[e], 8 * c + e < a.rot ? y[e] * sn[e] : 0.f);
+              for (int e = 0; e < 4; ++e) x[e] = f32x2_fma(x[e], cs[e], f32x2_mul(y[e], sn[e]));
+            } else {                          // dims behind rot_dim stay, whatever their neighbours hold
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (8 * c + 2 * e < a.rot) x[e] = f32x2_fma(x[e], cs[e], f32x2_mul(y[e], sn[e]));
+            }
+          }
+        }
+        if (live && h + b * kPer < hb) {
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f32x2_unpack(x[e], f[2 * e], f[2 * e + 1]);
+          if (dst != nullptr) Chunk8<bf16>::store(dst + b * step, f);
+          if (cdst != nullptr)
+            store_cache8(cdst + static_cast<int64_t>(b * kPer) * cache_head, f,
+                         scale != nullptr ? 1.f / scale[own + b * kPer] : 1.f);
         }
       }
-      if (!on) continue;
-      if (is_q) {
-        Chunk8<bf16>::store(a.q_out + t * a.q_stride + static_cast<int64_t>(hh) * a.d + 8 * c, x);
-        continue;
-      }
-      const int kvh = hh - a.hq - (is_v ? a.hkv : 0);
-      if (!is_v && a.k_out != nullptr)
-        Chunk8<bf16>::store(a.k_out + t * a.k_stride + static_cast<int64_t>(kvh) * a.d + 8 * c, x);
-      if (cache_row >= 0) {
-        const float* scale = is_v ? a.v_scale : a.k_scale;
-        store_cache8(static_cast<E*>(is_v ? a.vc : a.kc) + cache_row + static_cast<int64_t>(kvh) * a.page_size * a.d + 8 * c,
-                     x, scale != nullptr ? 1.f / scale[kvh] : 1.f);
-      }
+      own += kRopeBatch * kPer;
+      if (dst != nullptr) dst += kRopeBatch * step;
+      if (cdst != nullptr) cdst += static_cast<int64_t>(kRopeBatch * kPer) * cache_head;
     }
-  }
+  };
+  using Turned = std::integral_constant<bool, false>;
+  using Value = std::integral_constant<bool, true>;
+  const int qk = a.hq + a.hkv;
+  E* kc = cache_row < 0 ? nullptr : static_cast<E*>(a.kc);
+  section(Turned{}, h0, min(h1, a.hq), 0, a.q_gain, a.q_out + t * a.q_stride, static_cast<E*>(nullptr), nullptr);
+  if (kc != nullptr || a.k_out != nullptr)
+    section(Turned{}, max(h0, a.hq), min(h1, qk), a.hq, a.k_gain, a.k_out == nullptr ? nullptr : a.k_out + t * a.k_stride, kc,
+            a.k_scale);
+  if (kc != nullptr)
+    section(Value{}, max(h0, qk), h1, qk, nullptr, static_cast<bf16*>(nullptr), static_cast<E*>(a.vc), a.v_scale);
 }
 
 template <typename E, int LP> cudaError_t rope_go(RopeArgs a, int num_sms, cudaStream_t st) {
@@ -379,23 +437,34 @@ cudaError_t kv_slots_launch(const int32_t* len_before, const int32_t* n_new, int
         kv_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
+  PageDiv div;
+  div.P = page_size;
+  div.shift = 31;
+  while ((1 << (div.shift - 31)) < page_size) ++div.shift;
+  div.mul = static_cast<uint32_t>(((1ull << div.shift) + page_size - 1) / page_size);
+  // One CTA for a step's few tokens; a run of tokens per thread over many CTAs
+  // for prompts (251k tokens of 1000 requests: 25.8 us on one cluster of eight
+  // CTAs); one cluster when the lengths advance in place.
+  const int64_t runs = (static_cast<int64_t>(T) + kSlotRun - 1) / kSlotRun;
+  const bool in_place = len_after == len_before || used_after == used_before;
+  const int threads = n > 4096 ? 1024 : 256;
+  int ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(148, (runs + threads - 1) / threads)));
   cudaLaunchConfig_t cfg = {};
-  // one CTA until its threads have more than one run of tokens each
-  const int ctas = T > kSlotRun * kSlotThreads ? 8 : 1;
-  const bool wide = ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slots)) & 15) == 0;
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kSlotThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  const bool cluster = in_place && ctas > 1;
+  if (cluster) attr[0].val.clusterDim.x = ctas = 8;
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(cluster ? 1024 : threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_slots_kernel, len_before, n_new, n, page_size, free_pages,
-                            n_free, used_before, block_table, stride, T, offsets, positions, slots,
-                            len_after, used_after, unserved, wide);
+  cfg.numAttrs = cluster ? 1 : 0;
+  const bool wide = ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slots)) & 15) == 0;
+  return cudaLaunchKernelEx(&cfg, kv_slots_kernel, len_before, n_new, n, div, free_pages, n_free,
+                            used_before, block_table, stride, T, offsets, positions, slots,
+                            len_after, used_after, unserved, wide, cluster);
 }
 
 cudaError_t qk_norm_rope_launch(const void* qkv, int64_t qkv_stride, void* q_out, int64_t q_stride,
@@ -420,6 +489,7 @@ cudaError_t qk_norm_rope_launch(const void* qkv, int64_t qkv_stride, void* q_out
   a.q_gain = q_gain;
   a.k_gain = k_gain;
   a.eps = eps;
+  a.inv_d = 1.f / static_cast<float>(d);
   a.freqs = rope.freqs;
   a.rot = rope.rot_dim;
   a.interleaved = rope.layout;

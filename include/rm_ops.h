@@ -253,9 +253,10 @@ int rm_op_attention_noalloc(const void* qkv, void* ctx, const int32_t* offsets, 
  * Unlike the steps above, these take grouped heads (n_q_heads a multiple of
  * n_kv_heads; query head j reads key-value head j / (n_q_heads / n_kv_heads))
  * and rows with a pitch (row_stride elements from one token to the next).
- * Every device pointer must belong to the current CUDA device (RM_E_INVAL
- * otherwise, host memory included).  None of them allocates or keeps anything
- * between calls; all can be captured in a CUDA graph.
+ * Every device pointer must belong to the current CUDA device; an output
+ * pointer that does not (host memory, or another device's) gives RM_E_INVAL.
+ * None of them allocates or keeps anything between calls; all can be captured
+ * in a CUDA graph.
  * ------------------------------------------------------------------------- */
 
 /* A paged cache.  Element (page p, kv head h, slot s, dim c) of the keys is
@@ -372,7 +373,7 @@ int rm_op_qk_norm_rope(const void* qkv, int64_t qkv_stride, void* q_out, int64_t
  * sums are taken before that rounding).  q, out: [T][n_q_heads*head_dim], k,
  * v: [T][n_kv_heads*head_dim], bf16, each with its row stride; offsets: DEVICE
  * int32[n_seqs+1], offsets[0] = 0, non-decreasing (empty sequences allowed),
- * offsets[n_seqs] <= T; rows behind it are neither read nor written.  Values
+ * offsets[n_seqs] <= T; rows behind it are not written.  Values
  * and keys that a row does not see do not reach it, infinities and NaN among
  * them.  head_dim 64 or 128; pointers 16-byte aligned, strides multiples of 8
  * elements; n_q_heads / n_kv_heads <= 128. */
