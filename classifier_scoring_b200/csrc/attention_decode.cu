@@ -13,8 +13,10 @@
 //  - each warp of a CTA takes its own keys of every tile through a private
 //    ring of cp.async stages, with no barrier between warps until a unit ends;
 //    the ring runs across unit borders.
-//  - the query heads that share a kv head are the rows of one mma.sync tile
-//    (m16n8k16), so a key is read once for all of them.
+//  - the query heads that share a kv head are the columns of mma.sync tiles
+//    (m16n8k16: 16 keys by 8 heads for the scores, 16 dims by 8 heads for the
+//    output), so a key is read once for all of them and a step's arithmetic
+//    follows the head count, eight at a time.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -27,27 +29,30 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 16;                       // query heads per unit (rows of an MMA tile)
+constexpr int kUnitCost = 2;                    // a unit's beginning and end, in tiles
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxCtas = 148 * kCtasPerSm;      // the workspace has parts for this many
 
-// Keys per warp and step, and ring depth: a stage holds 8 KB of keys and
-// values (4 KB for 8-bit heads of 64), and two CTAs fit an SM.
-template <int D, typename E> struct Shape {
+// NH columns of eight query heads per unit.  Keys per warp and step, and ring
+// depth: a stage holds 8 KB of keys and values (4 KB for 8-bit heads of 64),
+// and two CTAs fit an SM.
+template <int D, typename E, int NH> struct Shape {
+  static constexpr int kRows = 8 * NH;                  // query heads of a unit
   static constexpr int kKeys = D * sizeof(E) >= 256 ? 16 : 32;
   static constexpr int kTile = kWarps * kKeys;
   static constexpr int kRowBytes = D * sizeof(E);
   static constexpr int kHalf = kKeys * kRowBytes;       // the keys of a stage; its values follow
   static constexpr int kStages = 2 * kHalf >= 8192 ? 3 : 6;
   static constexpr int kRing = kWarps * kStages * 2 * kHalf;
-  static constexpr int kSum = kRing;                    // float [kRows][D]
-  static constexpr int kMl = kSum + kRows * D * 4;      // float [kWarps][kRows][2]
+  static constexpr int kPitch = D + 4;                  // of a head's sums: heads 2t in different banks
+  static constexpr int kSum = kRing;                    // float [kRows][kPitch]
+  static constexpr int kMl = kSum + kRows * kPitch * 4; // float [kWarps][kRows][2]
   static constexpr int kSmem = kMl + kWarps * kRows * 2 * 4;
 };
 
 struct Parts {            // workspace
-  float* o;               // [ctas][2][kRows][D]
-  float* ml;              // [ctas][2][kRows][2]
+  float* o;               // [ctas][2][rows][D]
+  float* ml;              // [ctas][2][rows][2]
   int4* rec;              // [ctas]: unit that begins in the CTA's stretch and goes on behind it
 };
 
@@ -69,7 +74,7 @@ struct DecodeArgs {
   bf16* out;
   int64_t out_stride;
   float scale_log2;
-  int units;                    // per sequence: hkv * ceil(group / kRows)
+  int units;                    // per sequence: hkv * ceil(group / rows of a unit)
   Parts parts;
 };
 
@@ -92,13 +97,18 @@ __device__ __forceinline__ Seen seen_of(const DecodeArgs& a, int s, int tile) {
   return r;
 }
 
-// Position in the laid-out tiles: sequence, unit of it, key tile of that.
+// Position in the laid-out tiles: sequence, unit of it, key tile of that, and
+// the tile's place v.  A unit takes kUnitCost places before its first tile, so
+// that stretches of many short units are no slower than others.
 struct Cursor {
   int s, u, t;
+  long long v;
   Seen seen;
   __device__ __forceinline__ void next(const DecodeArgs& a, int tile) {
+    ++v;
     if (++t < seen.nt) return;
     t = 0;
+    v += kUnitCost;
     if (++u < a.units) return;
     u = 0;
     if (++s < a.n) seen = seen_of(a, s, tile);
@@ -129,10 +139,21 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// two e4m3 bytes (low half of x) as two fp16
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t x) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x & 0xffffu), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// four e4m3 bytes as fp16: bytes 0 and 1 in lo, 2 and 3 in hi
+__device__ __forceinline__ void e4m3x4_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
+}
+// the transpose of the 8 x 8 matrix of 16-bit elements that a warp holds, row
+// lane / 4, columns 2 (lane % 4) and one more
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -144,24 +165,25 @@ template <int RowBytes> __device__ __forceinline__ int chunk_at(int r, int c) {
   return RowBytes >= 128 ? r * RowBytes + ((c ^ (r & 7)) << 4) : r * RowBytes + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-template <int D, typename E>
+template <int D, typename E, int NH>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const DecodeArgs a) {
-  using SH = Shape<D, E>;
+  using SH = Shape<D, E, NH>;
   constexpr bool kF8 = sizeof(E) == 1;
-  constexpr int kKeys = SH::kKeys, kStages = SH::kStages;
+  constexpr int kKeys = SH::kKeys, kStages = SH::kStages, kRows = SH::kRows, kPitch = SH::kPitch;
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ long long scan[kWarps];
   __shared__ int start_s;
   __shared__ long long start_rem;
   __shared__ uint32_t masks[kWarps][kStages];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_launch_dependents();
 
-  // this CTA's stretch [t0, t1) of all tiles, and where it begins
+  // this CTA's stretch [v0, v1) of all places, and where it begins
   const int per = (a.n + kThreads - 1) / kThreads;
   const int i0 = min(a.n, tid * per), i1 = min(a.n, i0 + per);
+  auto places = [&](int i) { return static_cast<long long>(seen_of(a, i, SH::kTile).nt + kUnitCost) * a.units; };
   long long mine = 0;
-  for (int i = i0; i < i1; ++i) mine += static_cast<long long>(seen_of(a, i, SH::kTile).nt) * a.units;
+  for (int i = i0; i < i1; ++i) mine += places(i);
   long long upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -178,16 +200,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   }
   const int c = blockIdx.x;
   const long long ctas = min(static_cast<long long>(gridDim.x), total);   // no empty stretch among these
-  if (c >= ctas) {
-    if (tid == 0) a.parts.rec[c] = make_int4(-1, 0, 0, 0);
-    return;
-  }
-  const long long t0 = c * total / ctas, t1 = (c + 1) * total / ctas;
-  if (t0 >= upto - mine && t0 < upto) {
-    long long rem = t0 - (upto - mine);
+  const long long v0 = c < ctas ? c * total / ctas : total, v1 = c < ctas ? (c + 1) * total / ctas : total;
+  if (v0 < v1 && v0 >= upto - mine && v0 < upto) {
+    long long rem = v0 - (upto - mine);
     int i = i0;
     for (;; ++i) {
-      const long long k = static_cast<long long>(seen_of(a, i, SH::kTile).nt) * a.units;
+      const long long k = places(i);
       if (rem < k) break;
       rem -= k;
     }
@@ -196,12 +214,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   }
   __syncthreads();
   Cursor use;
-  use.s = start_s;
-  use.seen = seen_of(a, use.s, SH::kTile);
-  use.u = static_cast<int>(start_rem / use.seen.nt);
-  use.t = static_cast<int>(start_rem % use.seen.nt);
+  use.v = v1;                                   // an empty stretch
+  if (v0 < v1) {
+    use.s = start_s;
+    use.seen = seen_of(a, use.s, SH::kTile);
+    const int len = use.seen.nt + kUnitCost;
+    use.u = static_cast<int>(start_rem / len);
+    const int at = static_cast<int>(start_rem % len);
+    use.t = max(0, at - kUnitCost);
+    use.v = v0 + max(0, kUnitCost - at);        // the first place of the stretch that holds a tile
+  }
+  if (use.v >= v1) {
+    if (tid == 0) a.parts.rec[c] = make_int4(-1, 0, 0, 0);
+    return;
+  }
   Cursor get = use;
-  const int steps = static_cast<int>(t1 - t0);
+  const long long first = use.v;
   const int group = a.hq / a.hkv, mtiles = a.units / a.hkv;
 
   uint8_t* ring = sm + warp * kStages * 2 * SH::kHalf;
@@ -212,10 +240,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   // The page of a lane's key is looked up one step before its rows are
   // fetched.
   int pg = -1;
+  bool got = false;                             // a step is looked up
   int64_t row_in_page = 0;
-  auto lookup = [&](bool more) {
+  auto lookup = [&]() {
     pg = -1;
-    if (!more) return;
+    got = get.v < v1;
+    if (!got) return;
     const unsigned j = static_cast<unsigned>(get.t) * SH::kTile + warp * kKeys + lane;
     if (lane < kKeys && j < static_cast<unsigned>(get.seen.vis)) {
       const int key = static_cast<int>(j) + (j < static_cast<unsigned>(get.seen.nsink) ? 0 : get.seen.skip);
@@ -227,162 +257,184 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   };
   auto fetch = [&](int stage) {
     const bool ok = pg >= 0 && pg < a.n_pages;
-    const int64_t at = ok ? pg * a.page_stride + row_in_page * D : 0;
+    const int64_t at = ok ? (pg * a.page_stride + row_in_page * D) * static_cast<int64_t>(sizeof(E)) : 0;
     const uint32_t mask = __ballot_sync(0xffffffffu, ok);
     if (lane == 0) masks[warp][stage] = mask;
     const uint32_t dst = ring_u + stage * 2 * SH::kHalf;
     constexpr int kChunks = SH::kRowBytes / 16;
-    const char* kb = static_cast<const char*>(a.kc);
-    const char* vb = static_cast<const char*>(a.vc);
+    const char* kb = static_cast<const char*>(a.kc) + (lane % kChunks) * 16;
+    const char* vb = static_cast<const char*>(a.vc) + (lane % kChunks) * 16;
 #pragma unroll
     for (int i = 0; i < kKeys * kChunks / 32; ++i) {
-      const int r = (i * 32 + lane) / kChunks, ch = (i * 32 + lane) % kChunks;
-      const int64_t off = __shfl_sync(0xffffffffu, at, r) * static_cast<int64_t>(sizeof(E)) + ch * 16;
+      const int r = i * (32 / kChunks) + lane / kChunks;
+      const int64_t off = __shfl_sync(0xffffffffu, at, r);
       const int bytes = (mask >> r) & 1 ? 16 : 0;               // 0: the row is filled with zeros
-      const uint32_t d = dst + chunk_at<SH::kRowBytes>(r, ch);
+      const uint32_t d = dst + chunk_at<SH::kRowBytes>(r, lane % kChunks);
       cp16(d, kb + off, bytes);
       cp16(d + SH::kHalf, vb + off, bytes);
     }
   };
 
-  uint32_t qf[D / 16][4];
-  float sc[2], o[D / 8][4], m[2], l[2];
+  // The lane's heads are columns 8 nh + 2t, + 1 (t = lane % 4) of the scores
+  // and the output; the query operand holds head 8 nh + lane / 4.
+  const int g = lane >> 2, t2 = (lane & 3) * 2;
+  uint32_t qf[NH][D / 16][2];
+  float sc[NH][2], m[NH][2], l[NH][2], o[D / 16][NH][4];
   auto begin_unit = [&]() {
     const int h = use.u / mtiles, r0 = (use.u % mtiles) * kRows;
     const int rows = min(kRows, group - r0);
     const bf16* q = a.q + use.s * a.q_stride + static_cast<int64_t>(h * group + r0) * D;
-    const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int r = g + (x & 1) * 8;
-        // 8-bit keys arrive four dims to a lane: dims 4t..4t+3 of a step are
-        // the MMA's k = 2t, 2t+1, 2t+8, 2t+9, for the query as for the keys
-        const int dim = ks * 16 + (kF8 ? 4 * t + (x >> 1) * 2 : 2 * t + (x >> 1) * 8);
-        qf[ks][x] = r < rows ? *reinterpret_cast<const uint32_t*>(q + r * D + dim) : 0u;
-      }
     const float ks = a.scale_log2 * (kF8 && a.k_scale != nullptr ? a.k_scale[h] : 1.f);
-    sc[0] = sc[1] = ks;
-    if (kF8) {
-      // bf16 queries as fp16, times the power of two that brings the row's
-      // largest to [2^13, 2^14): exact but for entries 2^-27 below it
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+    for (int nh = 0; nh < NH; ++nh) {
+      const int r = nh * 8 + g;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          // 8-bit keys arrive four dims to a lane: dims 4t..4t+3 of a step are
+          // the MMA's k = 2t, 2t+1, 2t+8, 2t+9, for the query as for the keys
+          const int dim = k * 16 + (kF8 ? 2 * t2 + x * 2 : t2 + x * 8);
+          qf[nh][k][x] = r < rows ? *reinterpret_cast<const uint32_t*>(q + r * D + dim) : 0u;
+        }
+      sc[nh][0] = sc[nh][1] = ks;
+      if (kF8) {
+        // bf16 queries as fp16, times the power of two that brings the head's
+        // largest to [2^13, 2^14): exact but for entries 2^-27 below it
         float top = 0.f;
 #pragma unroll
-        for (int k2 = 0; k2 < D / 16; ++k2)
-          top = fmaxf(top, fmaxf(fmaxf(fabsf(bf16_lo(qf[k2][x])), fabsf(bf16_hi(qf[k2][x]))),
-                                 fmaxf(fabsf(bf16_lo(qf[k2][x + 2])), fabsf(bf16_hi(qf[k2][x + 2])))));
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) top = fmaxf(top, fmaxf(fabsf(bf16_lo(qf[nh][k][x])), fabsf(bf16_hi(qf[nh][k][x]))));
         top = group_max<4>(top);
         const int e = top > 0.f && top < INFINITY ? 13 - ilogbf(top) : 0;
-        sc[x] = ldexpf(ks, -e);
+        // 2^e as two factors: e may pass the exponents of fp32
+        const float f0 = ldexpf(1.f, e >> 1), f1 = ldexpf(1.f, e - (e >> 1));
 #pragma unroll
-        for (int k2 = 0; k2 < D / 16; ++k2) {
-          qf[k2][x] = pack_f16x2(ldexpf(bf16_lo(qf[k2][x]), e), ldexpf(bf16_hi(qf[k2][x]), e));
-          qf[k2][x + 2] = pack_f16x2(ldexpf(bf16_lo(qf[k2][x + 2]), e), ldexpf(bf16_hi(qf[k2][x + 2]), e));
-        }
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int x = 0; x < 2; ++x)
+            qf[nh][k][x] = pack_f16x2(bf16_lo(qf[nh][k][x]) * f0 * f1, bf16_hi(qf[nh][k][x]) * f0 * f1);
+        const float back = ldexpf(ks, -e);
+        sc[nh][0] = __shfl_sync(0xffffffffu, back, t2 * 4);
+        sc[nh][1] = __shfl_sync(0xffffffffu, back, t2 * 4 + 4);
       }
-    }
-    m[0] = m[1] = -INFINITY;
-    l[0] = l[1] = 0.f;
+      m[nh][0] = m[nh][1] = -INFINITY;
+      l[nh][0] = l[nh][1] = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      for (int i = 0; i < D / 16; ++i) o[i][nh][0] = o[i][nh][1] = o[i][nh][2] = o[i][nh][3] = 0.f;
+    }
   };
 
+  const int lr = lane & 7, lm = lane >> 3;
   auto step = [&](int stage) {
     const uint32_t kb = ring_u + stage * 2 * SH::kHalf, vb = kb + SH::kHalf;
-    const uint32_t mask = masks[warp][stage];
-    float s[kKeys / 8][4];
+    const uint32_t mask = masks[warp][stage] >> g;              // of keys g, g + 8, ...
+    float s[kKeys / 16][NH][4];
 #pragma unroll
-    for (int i = 0; i < kKeys / 8; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-    const int lr = lane & 7, lm = lane >> 3;
+    for (int kt = 0; kt < kKeys / 16; ++kt) {
 #pragma unroll
-    for (int nt = 0; nt < kKeys / 8; ++nt) {
+      for (int nh = 0; nh < NH; ++nh) s[kt][nh][0] = s[kt][nh][1] = s[kt][nh][2] = s[kt][nh][3] = 0.f;
+      const int kr = kt * 16 + (lm & 1) * 8 + lr;
       if (kF8) {
 #pragma unroll
-        for (int k4 = 0; k4 < D / 64; ++k4) {                    // four 16-dim steps a load
-          uint32_t b[4];
-          ldsm4(kb + chunk_at<SH::kRowBytes>(nt * 8 + lr, k4 * 4 + lm), b);
+        for (int k2 = 0; k2 < D / 32; ++k2) {                    // two 16-dim steps a load
+          uint32_t b[4], f[4];
+          ldsm4(kb + chunk_at<SH::kRowBytes>(kr, k2 * 2 + (lm >> 1)), b);
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            mma<E>(s[nt], qf[k4 * 4 + x], e4m3x2_f16x2(b[x]), e4m3x2_f16x2(b[x] >> 16));
+          for (int x = 0; x < 2; ++x) {
+            e4m3x4_f16(b[2 * x], f[0], f[2]);
+            e4m3x4_f16(b[2 * x + 1], f[1], f[3]);
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh) mma<E>(s[kt][nh], f, qf[nh][k2 * 2 + x][0], qf[nh][k2 * 2 + x][1]);
+          }
         }
       } else {
 #pragma unroll
-        for (int k2 = 0; k2 < D / 32; ++k2) {                    // two 16-dim steps a load
+        for (int k = 0; k < D / 16; ++k) {
           uint32_t b[4];
-          ldsm4(kb + chunk_at<SH::kRowBytes>(nt * 8 + lr, k2 * 4 + lm), b);
-          mma<E>(s[nt], qf[k2 * 2], b[0], b[1]);
-          mma<E>(s[nt], qf[k2 * 2 + 1], b[2], b[3]);
+          ldsm4(kb + chunk_at<SH::kRowBytes>(kr, k * 2 + (lm >> 1)), b);
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh) mma<E>(s[kt][nh], b, qf[nh][k][0], qf[nh][k][1]);
         }
       }
     }
-    // base-2 scores of the lane's rows lane/4 and lane/4 + 8, keys 8 nt + 2t + {0, 1}
-    const int t2 = (lane & 3) * 2;
-    float top[2] = {-INFINITY, -INFINITY};
+    // base-2 scores: elements 0, 1 of key 16 kt + g, 2, 3 of key 16 kt + 8 + g
 #pragma unroll
-    for (int nt = 0; nt < kKeys / 8; ++nt)
+    for (int nh = 0; nh < NH; ++nh) {
+      float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const bool in = (mask >> (nt * 8 + t2 + (x & 1))) & 1;
-        s[nt][x] = in ? s[nt][x] * sc[x >> 1] : -INFINITY;
-        top[x >> 1] = fmaxf(top[x >> 1], s[nt][x]);
-      }
-    top[0] = group_max<4>(top[0]);
-    top[1] = group_max<4>(top[1]);
-    // The reference the exponentials are taken against follows the maximum
-    // only when it falls 2^8 behind: a rescale of the output is then rare, and
-    // P stays below 2^8 with the same relative rounding.
-    if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
+      for (int kt = 0; kt < kKeys / 16; ++kt)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float mn = fmaxf(m[x], top[x]);
-        const float keep = m[x] == -INFINITY ? 0.f : ex2_approx_ftz(m[x] - mn);
-        m[x] = mn;
-        l[x] *= keep;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          o[i][2 * x] *= keep;
-          o[i][2 * x + 1] *= keep;
+        for (int x = 0; x < 4; ++x) {
+          const bool in = (mask >> (kt * 16 + (x >> 1) * 8)) & 1;
+          s[kt][nh][x] = in ? s[kt][nh][x] * sc[nh][x & 1] : -INFINITY;
+          top[x & 1] = fmaxf(top[x & 1], s[kt][nh][x]);
         }
+#pragma unroll
+      for (int w = 4; w < 32; w <<= 1) {
+        top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], w));
+        top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], w));
       }
+      // The reference the exponentials are taken against follows the maximum
+      // only when it falls 2^8 behind: a rescale of the output is then rare, and
+      // P stays below 2^8 with the same relative rounding.
+      if (__any_sync(0xffffffffu, top[0] > m[nh][0] + 8.f || top[1] > m[nh][1] + 8.f)) {
+        float keep[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float mn = fmaxf(m[nh][x], top[x]);
+          keep[x] = m[nh][x] == -INFINITY ? 0.f : ex2_approx_ftz(m[nh][x] - mn);
+          m[nh][x] = mn;
+          l[nh][x] *= keep[x];
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[i][nh][x] *= keep[x & 1];
+      }
+      const float ref[2] = {m[nh][0] == -INFINITY ? 0.f : m[nh][0], m[nh][1] == -INFINITY ? 0.f : m[nh][1]};
+#pragma unroll
+      for (int kt = 0; kt < kKeys / 16; ++kt)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          s[kt][nh][x] = ex2_approx_ftz(s[kt][nh][x] - ref[x & 1]);   // a masked key's is 2^-inf = 0
+          l[nh][x & 1] += s[kt][nh][x];
+        }
     }
-    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
-    for (int nt = 0; nt < kKeys / 8; ++nt)
+    for (int kt = 0; kt < kKeys / 16; ++kt) {
+      uint32_t p[NH][2];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const bool in = (mask >> (nt * 8 + t2 + (x & 1))) & 1;
-        s[nt][x] = in ? ex2_approx_ftz(s[nt][x] - ref[x >> 1]) : 0.f;
-        l[x >> 1] += s[nt][x];
-      }
+      for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-    for (int k16 = 0; k16 < kKeys / 16; ++k16) {
-      uint32_t p[4];
+        for (int x = 0; x < 2; ++x)
+          p[nh][x] = transposed(kF8 ? pack_f16x2(s[kt][nh][2 * x], s[kt][nh][2 * x + 1])
+                                    : pack_bf16x2(s[kt][nh][2 * x], s[kt][nh][2 * x + 1]));
+      if (kF8) {
+        const int vr = kt * 16 + (lm & 1) * 8 + lr;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float lo = s[2 * k16 + (x >> 1)][(x & 1) * 2], hi = s[2 * k16 + (x >> 1)][(x & 1) * 2 + 1];
-        p[x] = kF8 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
-      }
-      // matrices 0, 1: keys 0..7, 8..15 of the first 16-byte chunk; 2, 3: of the next
-      const int vr = k16 * 16 + (lm & 1) * 8 + lr;
+        for (int d2 = 0; d2 < D / 32; ++d2) {                    // two 16-dim tiles a load
+          uint32_t b[4], f[4];
+          ldsm4t(vb + chunk_at<SH::kRowBytes>(vr, d2 * 2 + (lm >> 1)), b);
 #pragma unroll
-      for (int c2 = 0; c2 < SH::kRowBytes / 32; ++c2) {
-        uint32_t b[4];
-        ldsm4t(vb + chunk_at<SH::kRowBytes>(vr, c2 * 2 + (lm >> 1)), b);
-        if (kF8) {
-          // a register holds dims 2c, 2c+1 of two keys: even dims make one
-          // 8-dim tile, odd dims the next
+          for (int x = 0; x < 2; ++x) {
+            // a register holds dims 2g, 2g+1 of two keys: the tile's rows
+            // 0..7 are the even dims, 8..15 the odd ones
+            e4m3x4_f16(__byte_perm(b[2 * x], 0, 0x3120), f[0], f[1]);
+            e4m3x4_f16(__byte_perm(b[2 * x + 1], 0, 0x3120), f[2], f[3]);
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint32_t b0 = __byte_perm(b[2 * y], 0, 0x3120), b1 = __byte_perm(b[2 * y + 1], 0, 0x3120);
-            mma<E>(o[c2 * 4 + y * 2], p, e4m3x2_f16x2(b0), e4m3x2_f16x2(b1));
-            mma<E>(o[c2 * 4 + y * 2 + 1], p, e4m3x2_f16x2(b0 >> 16), e4m3x2_f16x2(b1 >> 16));
+            for (int nh = 0; nh < NH; ++nh) mma<E>(o[d2 * 2 + x][nh], f, p[nh][0], p[nh][1]);
           }
-        } else {
-          mma<E>(o[c2 * 2], p, b[0], b[1]);
-          mma<E>(o[c2 * 2 + 1], p, b[2], b[3]);
+        }
+      } else {
+        const int vr = kt * 16 + (lm >> 1) * 8 + lr;
+#pragma unroll
+        for (int dt = 0; dt < D / 16; ++dt) {
+          uint32_t b[4];
+          ldsm4t(vb + chunk_at<SH::kRowBytes>(vr, dt * 2 + (lm & 1)), b);
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh) mma<E>(o[dt][nh], b, p[nh][0], p[nh][1]);
         }
       }
     }
@@ -390,48 +442,50 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
 
   // Joins the warps' states of a finished unit, in warp order, and writes the
   // output rows, or the unit's part when the stretch holds only part of it.
-  auto end_unit = [&](long long unit0) {
+  // As many warps as the buffer has room for write at once.
+  auto end_unit = [&](long long unit0, bool whole) {
     const int h = use.u / mtiles, r0 = (use.u % mtiles) * kRows;
     const int rows = min(kRows, group - r0);
-    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      l[x] = group_sum<4>(l[x]);
-      if (t == 0) {
-        ml[(warp * kRows + g + 8 * x) * 2] = m[x];
-        ml[(warp * kRows + g + 8 * x) * 2 + 1] = l[x];
-      }
-    }
-    __syncthreads();
-    float w[2];
+    for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      float mt = -INFINITY;
+      for (int x = 0; x < 2; ++x) {
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) mt = fmaxf(mt, ml[(i * kRows + g + 8 * x) * 2]);
-      w[x] = m[x] == -INFINITY ? 0.f : ex2_approx_ftz(m[x] - mt);
-      if (l[x] != l[x]) w[x] = l[x];                       // a NaN seen before any maximum
-    }
-    for (int i = 0; i < kWarps; ++i) {
-      if (warp == i) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (g + 8 * x >= rows) continue;
-          float* dst = sum + (g + 8 * x) * D;
-#pragma unroll
-          for (int n8 = 0; n8 < D / 8; ++n8)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int dim = kF8 ? (n8 >> 1) * 16 + 4 * t + 2 * e + (n8 & 1) : n8 * 8 + 2 * t + e;
-              const float v = o[n8][2 * x + e] * w[x];
-              dst[dim] = i == 0 ? v : dst[dim] + v;
-            }
+        for (int w = 4; w < 32; w <<= 1) l[nh][x] += __shfl_xor_sync(0xffffffffu, l[nh][x], w);
+        if (g == 0) {
+          ml[(warp * kRows + nh * 8 + t2 + x) * 2] = m[nh][x];
+          ml[(warp * kRows + nh * 8 + t2 + x) * 2 + 1] = l[nh][x];
         }
+      }
+    __syncthreads();
+    const int room = rows * 4 <= kRows ? 4 : (rows * 2 <= kRows ? 2 : 1);
+    for (int i = 0; i < kWarps; i += room) {
+      if (warp >= i && warp < i + room) {
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int r = nh * 8 + t2 + x;
+            if (r >= rows) continue;
+            float mt = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) mt = fmaxf(mt, ml[(k * kRows + r) * 2]);
+            float w = m[nh][x] == -INFINITY ? 0.f : ex2_approx_ftz(m[nh][x] - mt);
+            if (l[nh][x] != l[nh][x]) w = l[nh][x];              // a NaN seen before any maximum
+            float* dst = sum + ((warp - i) * rows + r) * kPitch;
+#pragma unroll
+            for (int dt = 0; dt < D / 16; ++dt)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int dim = dt * 16 + (kF8 ? 2 * g + y : 8 * y + g);
+                const float v = o[dt][nh][2 * y + x] * w;
+                dst[dim] = i == 0 ? v : dst[dim] + v;
+              }
+          }
       }
       __syncthreads();
     }
-    const bool whole = unit0 >= t0 && unit0 + use.seen.nt <= t1;
-    const int slot = unit0 <= t0 ? 0 : 1;
+    const int slot = unit0 + kUnitCost <= first ? 0 : 1;
     float* po = a.parts.o + static_cast<size_t>(c * 2 + slot) * kRows * D;
     float* pm = a.parts.ml + static_cast<size_t>(c * 2 + slot) * kRows * 2;
     const float vs = kF8 && a.v_scale != nullptr ? a.v_scale[h] : 1.f;
@@ -445,7 +499,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
         const float mk = ml[(k * kRows + r) * 2], lk = ml[(k * kRows + r) * 2 + 1];
         lt += mk == -INFINITY ? lk : lk * ex2_approx_ftz(mk - mt);
       }
-      const float x0 = sum[r * D + d2], x1 = sum[r * D + d2 + 1];
+      float x0 = 0.f, x1 = 0.f;
+      for (int k = 0; k < room; ++k) {
+        const float2 v = *reinterpret_cast<const float2*>(sum + (k * rows + r) * kPitch + d2);
+        x0 += v.x;
+        x1 += v.y;
+      }
       if (whole) {
         const float inv = lt == 0.f ? 0.f : vs / lt;
         *reinterpret_cast<uint32_t*>(a.out + use.s * a.out_stride + static_cast<int64_t>(h * group + r0 + r) * D + d2) =
@@ -461,39 +520,42 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     __syncthreads();
   };
 
-  lookup(steps > 0);
+  lookup();
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) {
-    if (i < steps) {
+    if (got) {
       fetch(i);
-      lookup(i + 1 < steps);
+      lookup();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   begin_unit();
   int stage = 0;
   int4 rec = make_int4(-1, 0, 0, 0);
-  for (int i = 0; i < steps; ++i) {
+  for (;;) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     __syncwarp();
-    if (i + kStages - 1 < steps) {
+    if (got) {
       fetch(stage == 0 ? kStages - 1 : stage - 1);           // the stage read one step ago
-      lookup(i + kStages < steps);
+      lookup();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     step(stage);
     stage = stage + 1 == kStages ? 0 : stage + 1;
     const bool last_of_unit = use.t + 1 == use.seen.nt;
-    if (last_of_unit || i + 1 == steps) {
-      const long long unit0 = t0 + i - use.t;
-      end_unit(unit0);
-      if (!last_of_unit && unit0 >= t0) {                     // goes on in the next stretches
-        const long long end = unit0 + use.seen.nt;
-        rec = make_int4(use.s, use.u, unit0 == t0 ? 0 : 1, static_cast<int>((end * ctas - 1) / total));
+    const bool last = last_of_unit ? use.v + 1 + kUnitCost >= v1 : use.v + 1 >= v1;
+    if (last_of_unit || last) {
+      const long long unit0 = use.v - use.t - kUnitCost;      // the unit's first place
+      const bool begins = unit0 + kUnitCost >= first;         // its first tile is in this stretch
+      end_unit(unit0, begins && last_of_unit);
+      if (!last_of_unit && begins) {                          // it goes on in the next stretches
+        const long long end = unit0 + kUnitCost + use.seen.nt;
+        rec = make_int4(use.s, use.u, unit0 + kUnitCost <= first ? 0 : 1, static_cast<int>((end * ctas - 1) / total));
       }
     }
+    if (last) break;
     use.next(a, SH::kTile);
-    if (last_of_unit && i + 1 < steps) begin_unit();
+    if (last_of_unit) begin_unit();
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (tid == 0) a.parts.rec[c] = rec;
@@ -503,13 +565,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
 // that begins in stretch c and goes on, if any.  kJoinSplit groups of D
 // threads take every kJoinSplit-th part, then add up in order.
 constexpr int kJoinThreads = 256;
-template <int D>
+template <int D, int NH>
 __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const DecodeArgs a, int f8) {
+  constexpr int kRows = 8 * NH;
   constexpr int kGroups = kJoinThreads / D;
   __shared__ float w[kMaxCtas];
   __shared__ float red[kGroups][D];
   __shared__ float rmax[kJoinThreads / 32], rsum[kJoinThreads / 32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_wait();
   const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
   const int4 rec = a.parts.rec[c];
   if (rec.x < 0) return;
@@ -553,17 +616,26 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const De
   }
 }
 
+constexpr int kMaxRows = 16;                    // query heads per unit
+
 Parts parts_at(void* workspace, int d) {
   Parts p;
   p.o = static_cast<float*>(workspace);
-  p.ml = p.o + static_cast<size_t>(kMaxCtas) * 2 * kRows * d;
-  p.rec = reinterpret_cast<int4*>(p.ml + static_cast<size_t>(kMaxCtas) * 2 * kRows * 2);
+  p.ml = p.o + static_cast<size_t>(kMaxCtas) * 2 * kMaxRows * d;
+  p.rec = reinterpret_cast<int4*>(p.ml + static_cast<size_t>(kMaxCtas) * 2 * kMaxRows * 2);
   return p;
 }
 
-template <int D, typename E> cudaError_t launch(const DecodeArgs& a, int grid, cudaStream_t st) {
-  using SH = Shape<D, E>;
-  auto kernel = attn_decode_kernel<D, E>;
+template <int D, typename E, int NH>
+cudaError_t launch(DecodeArgs a, int num_sms, cudaStream_t st) {
+  using SH = Shape<D, E, NH>;
+  const int group = a.hq / a.hkv;
+  a.units = a.hkv * ((group + SH::kRows - 1) / SH::kRows);
+  // no more CTAs than tiles of the longest possible contexts
+  const int64_t keys = static_cast<int64_t>(a.table_stride) * a.P;
+  const int64_t most = static_cast<int64_t>(a.n) * a.units * ((keys + SH::kTile - 1) / SH::kTile + kUnitCost);
+  const int grid = static_cast<int>(std::min<int64_t>(most, std::min(kMaxCtas, num_sms * kCtasPerSm)));
+  auto kernel = attn_decode_kernel<D, E, NH>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::kSmem);
   if (e != cudaSuccess) return e;
   kernel<<<grid, kThreads, SH::kSmem, st>>>(a);
@@ -571,14 +643,14 @@ template <int D, typename E> cudaError_t launch(const DecodeArgs& a, int grid, c
   if (e != cudaSuccess) return e;
   // the join starts while the first kernel drains and waits for it
   PdlScope pdl(true);
-  return launch_k(attn_decode_join_kernel<D>, dim3(grid, std::min(kRows, a.hq / a.hkv)), dim3(kJoinThreads), 0, st, a,
+  return launch_k(attn_decode_join_kernel<D, NH>, dim3(grid, std::min(SH::kRows, group)), dim3(kJoinThreads), 0, st, a,
                   static_cast<int>(sizeof(E) == 1));
 }
 
 }  // namespace
 
 size_t attn_decode_workspace(int, int, const rm_kv_cache& c) {
-  return static_cast<size_t>(kMaxCtas) * (2 * kRows * (c.head_dim + 2) * sizeof(float) + sizeof(int4));
+  return static_cast<size_t>(kMaxCtas) * (2 * kMaxRows * (c.head_dim + 2) * sizeof(float) + sizeof(int4));
 }
 
 cudaError_t attn_decode_launch(const void* q, int64_t q_stride, const rm_kv_cache& c,
@@ -613,16 +685,15 @@ cudaError_t attn_decode_launch(const void* q, int64_t q_stride, const rm_kv_cach
   a.out = static_cast<bf16*>(out);
   a.out_stride = out_stride;
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(c.head_dim));
-  const int group = hq / c.n_kv_heads;
-  a.units = c.n_kv_heads * ((group + kRows - 1) / kRows);
   a.parts = parts_at(workspace, c.head_dim);
-  // no more CTAs than tiles of the longest possible contexts
-  const int64_t most = static_cast<int64_t>(n) * a.units *
-                       std::max<int64_t>(1, (static_cast<int64_t>(table_stride) * c.page_size + 63) / 64);
-  const int grid = static_cast<int>(std::min<int64_t>(most, std::min(kMaxCtas, num_sms * kCtasPerSm)));
-  using F8 = __nv_fp8_e4m3;
-  if (c.dtype == RM_E4M3) return c.head_dim == 64 ? launch<64, F8>(a, grid, st) : launch<128, F8>(a, grid, st);
-  return c.head_dim == 64 ? launch<64, bf16>(a, grid, st) : launch<128, bf16>(a, grid, st);
+  // up to eight query heads a kv head: one column tile, half the arithmetic
+  const bool few = hq / c.n_kv_heads <= 8;
+  auto go = [&](auto elem) {
+    using E = decltype(elem);
+    if (c.head_dim == 64) return few ? launch<64, E, 1>(a, num_sms, st) : launch<64, E, 2>(a, num_sms, st);
+    return few ? launch<128, E, 1>(a, num_sms, st) : launch<128, E, 2>(a, num_sms, st);
+  };
+  return c.dtype == RM_E4M3 ? go(__nv_fp8_e4m3{}) : go(bf16{});
 }
 
 }  // namespace rmk
