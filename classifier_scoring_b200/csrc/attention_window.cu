@@ -15,24 +15,24 @@
 // the item's keys are one range of packed rows, plus the first sequence's
 // sinks when its window has left them behind.  Items are dealt to one
 // persistent CTA per SM, the last tokens (which see most) first:
-//   warp 9, one lane : TMA -- the two Q tiles of an item and, per 128-key
-//                      chunk, K and V through a ring of slots (128-byte
-//                      swizzle, rows past the batch read as zeros);
-//   warp 8, one lane : tcgen05.mma, per chunk and tile X: O_X += P_X V of the
-//                      previous chunk, then S_X = Q_X K^T into the columns
-//                      that P_X just left (the tensor pipe runs its MMAs in
-//                      order).  While one tile's softmax runs, the other
-//                      tile's MMAs do.  K chunks of fewer keys take fewer
-//                      columns; chunks that a tile does not see are skipped;
-//   warps 0..7       : softmax, four warps a tile, one row per thread: the row
-//                      of S in registers, its maximum, the exponentials with
-//                      the scale folded into one packed FMA, P as bf16 back to
-//                      tensor memory.  The reference of the exponentials
-//                      follows the maximum only when it falls 2^8 behind, and
-//                      only then is O rescaled (in tensor memory, by the same
-//                      thread); chunks that a warp's rows admit in full take no
-//                      masks.  After the last chunk the thread reads its row
-//                      of O, divides and stores it.
+//   warp 10 : plans items ahead of the others: key range, chunks and the start of
+//             each row's sequence (searches in the offsets) into shared memory;
+//   warp 9  : TMA -- the two Q tiles of an item and, per 128-key chunk, K and V
+//             through a ring of slots (128-byte swizzle, rows past the batch
+//             read as zeros);
+//   warp 8  : tcgen05.mma, per chunk and tile X: O_X += P_X V of the previous
+//             chunk, then S_X = Q_X K^T into the columns that P_X just left
+//             (the tensor pipe runs its MMAs in order).  While one tile's
+//             softmax runs, the other tile's MMAs do.  K chunks of fewer keys
+//             take fewer columns; chunks that a tile does not see are skipped;
+//   warps 0..7 : softmax, four warps a tile, one row per thread, 64 keys at a
+//             time: the exponentials with the scale folded into one packed FMA,
+//             against a reference that follows the row's maximum only when that
+//             is 2^8 ahead (then O is rescaled in tensor memory by the same
+//             thread), so that no exponential waits for a maximum; P as bf16
+//             back to tensor memory.  32-key groups that every row of a warp
+//             admits take no masks, those that none admits are skipped.  After
+//             the last chunk the thread reads its row of O, divides, stores.
 // Tensor memory: S_0, S_1 (P over them), O_0, O_1: 512 columns for d = 128.
 //
 // A masked key has P = 0, but 0 times an infinity or NaN in its V row would
@@ -56,8 +56,22 @@ namespace {
 __device__ int32_t g_window_err[ERR_WORDS];
 
 constexpr int kTile = 128;              // rows of a tile, keys of a chunk
-constexpr int kThreads = 320;           // 8 softmax warps, MMA, TMA
+constexpr int kThreads = 384;           // 8 softmax warps; MMA, TMA and two idle ones
+// registers of the two kinds of warps; at launch every warp has 168 (the most
+// that three warps a scheduler allow), and 8 x 200 + 4 x 104 = 12 x 168
+constexpr int kSoftmaxRegs = 200, kIssueRegs = 104;
+constexpr int kPlans = 3;               // items planned ahead
 constexpr unsigned long long kLimitNs = 10000000000ull;
+
+// A work item: kv head; first token and token counts of its tiles; start of
+// the sequence of a tile's first token, and that token's first key inside its
+// window.
+struct Plan {
+  int h;                                // -1: no more items
+  int t0, count[2];
+  int start[2], lo[2];
+  uint8_t begins[2 * kTile];            // per token: its sequence's start - t0, 0 = at or before t0
+};
 
 template <int D> struct Smem {
   static constexpr int kBox = kTile * 128;                 // 64 dims of 128 rows
@@ -66,10 +80,12 @@ template <int D> struct Smem {
   static constexpr int kQ = 0;
   static constexpr int kKv = 2 * kBuf;
   static constexpr int kBar = kKv + kSlots * kBuf;
-  // q_full[2] q_empty[2] s_full[2] p_full[2] o_full[2] kv_full[] kv_empty[]
-  static constexpr int kBars = 10 + 2 * kSlots;
+  // q_full[2] q_empty[2] s_full[2] p_full[2] o_full[2] plan_full[] plan_empty[]
+  // kv_full[] kv_empty[]
+  static constexpr int kBars = 10 + 2 * kPlans + 2 * kSlots;
   static constexpr int kTmemSlot = kBar + kBars * 8;
-  static constexpr int kBytes = kTmemSlot + 16 + 1024;     // + 1024-byte alignment slack
+  static constexpr int kPlan = kTmemSlot + 16;
+  static constexpr int kBytes = kPlan + kPlans * static_cast<int>(sizeof(Plan)) + 1024;   // + alignment slack
   static_assert(kBytes <= 232448, "fits one CTA's shared memory");
 };
 
@@ -82,20 +98,40 @@ struct WindowArgs {
   float scale_log2;
 };
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// The issuing roles run as whole warps, whose control flow and operands stay
+// uniform (a branch on the lane would cost moves to uniform registers around
+// every instruction: 85 to 140 cycles an MMA instead of its 64); the one lane
+// that issues is a predicate of the instruction.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ int uni(int x) { return __reduce_max_sync(0xffffffffu, x); }
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar),
+      "r"(lead)
       : "memory");
 }
 // MN-major operand (V as it lies: rows of keys, 64 dims of 128 bytes, 128-byte
@@ -114,41 +150,21 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
   return false;
 }
 
-// Where a token's keys begin: its sequence and its window.
-struct Row {
-  int start, lo;
-};
-__device__ __forceinline__ Row row_of(const WindowArgs& a, int t) {
-  Row r;
-  r.start = a.offsets[upper_index(a.offsets, a.n, t)];
-  r.lo = a.window > 0 ? max(r.start, t - a.window + 1) : r.start;
-  return r;
+// the same for a whole warp: all lanes leave with one answer
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait(bar, parity));
 }
 
-// A work item's tiles and key chunks.  Chunks 0..nsink_chunks-1 cover the
-// sinks [start, start + nsink) of the first row's sequence that lie before
-// the window of every row; the others [lo, hi).
-struct Item {
-  int h, t0[2], t1[2];            // kv head; tokens of the tiles (t1 = t0: none)
-  int start, sinks, nsink, lo, hi, nsc, nc;
-  Row first[2];                   // the tiles' first rows
-  __device__ __forceinline__ bool load(const WindowArgs& a, int item, int end) {
-    const int pairs = a.items / a.hkv;
-    h = item % a.hkv;
-    t0[0] = (pairs - 1 - item / a.hkv) * 2 * a.tq;
-    if (t0[0] >= end) return false;
-    t1[0] = t0[1] = min(t0[0] + a.tq, end);
-    t1[1] = min(t0[1] + a.tq, end);
-    first[0] = first[1] = row_of(a, t0[0]);
-    if (t1[1] > t0[1]) first[1] = row_of(a, t0[1]);
-    start = first[0].start;
-    lo = first[0].lo;
-    hi = t1[1];
-    sinks = a.sinks;
-    nsink = min(sinks, lo - start);
+// An item's key chunks.  Chunks 0..nsc-1 cover the sinks [start, start +
+// nsink) of the first token's sequence that lie before the window of every
+// row; the others [lo, hi).
+struct Chunks {
+  int start, nsink, nsc, lo, hi, nc;
+  __device__ __forceinline__ Chunks(const WindowArgs& a, const Plan& p)
+      : start(uni(p.start[0])), lo(uni(p.lo[0])), hi(uni(p.t0 + p.count[0] + p.count[1])) {
+    nsink = min(a.sinks, lo - start);
     nsc = (nsink + kTile - 1) / kTile;
     nc = nsc + (hi - lo + kTile - 1) / kTile;
-    return true;
   }
   __device__ __forceinline__ int base(int c) const {
     return c < nsc ? start + c * kTile : lo + (c - nsc) * kTile;
@@ -156,14 +172,19 @@ struct Item {
   __device__ __forceinline__ int keys(int c) const {
     return min(kTile, c < nsc ? nsink - c * kTile : hi - base(c));
   }
-  // whether some row of tile x may see chunk c (its later rows see no earlier
-  // keys than its first, but for the sinks of sequences that begin in the
-  // tile, which are later still), and the tile's last chunk
-  __device__ __forceinline__ bool sees(int x, int c) const {
-    const int b = base(c), e = b + keys(c);
-    return t1[x] > t0[x] && b < t1[x] && (e > first[x].lo || (b - first[x].start < sinks && e > first[x].start));
+};
+// A tile's tokens [t0, t1) and what of the chunks it may see: its later rows
+// see no earlier keys than its first, but for the sinks of sequences that
+// begin in the tile, which are later still.
+struct Tile {
+  int t0, t1, start, lo;
+  __device__ __forceinline__ Tile(const Plan& p, int x)
+      : t0(uni(p.t0 + (x == 0 ? 0 : p.count[0]))), t1(uni(p.t0 + p.count[0] + (x == 0 ? 0 : p.count[1]))),
+        start(uni(p.start[x])), lo(uni(p.lo[x])) {}
+  __device__ __forceinline__ bool sees(const WindowArgs& a, int b, int keys) const {
+    return t1 > t0 && b < t1 && (b + keys > lo || (b - start < a.sinks && b + keys > start));
   }
-  __device__ __forceinline__ int last(int x) const { return nsc + (t1[x] - 1 - lo) / kTile; }
+  __device__ __forceinline__ int last(const Chunks& c) const { return c.nsc + (t1 - 1 - c.lo) / kTile; }
 };
 
 template <int D>
@@ -182,8 +203,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto s_full = [&](int x) { return bar0 + 8u * (4 + x); };
   auto p_full = [&](int x) { return bar0 + 8u * (6 + x); };
   auto o_full = [&](int x) { return bar0 + 8u * (8 + x); };
-  auto kv_full = [&](int s) { return bar0 + 8u * (10 + s); };
-  auto kv_empty = [&](int s) { return bar0 + 8u * (10 + NS + s); };
+  auto plan_full = [&](int e) { return bar0 + 8u * (10 + e); };
+  auto plan_empty = [&](int e) { return bar0 + 8u * (10 + kPlans + e); };
+  auto kv_full = [&](int s) { return bar0 + 8u * (10 + 2 * kPlans + s); };
+  auto kv_empty = [&](int s) { return bar0 + 8u * (10 + 2 * kPlans + NS + s); };
+  Plan* plans = reinterpret_cast<Plan*>(sm + SL::kPlan);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + SL::kTmemSlot);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -194,6 +218,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s_full(x), 1);
       mbar_init(p_full(x), 4);           // the tile's four warps
       mbar_init(o_full(x), 1);
+    }
+    for (int e = 0; e < kPlans; ++e) {
+      mbar_init(plan_full(e), 1);
+      mbar_init(plan_empty(e), 10);      // the warps that go by plans
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(kv_full(s), 1);
@@ -213,248 +241,419 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   auto s_at = [&](int x) { return tmem + static_cast<uint32_t>(x * kTile); };
   auto o_at = [&](int x) { return tmem + static_cast<uint32_t>(2 * kTile + x * kTile); };
-  const int end = a.offsets[a.n];
-  Item it;
+  // the next plan, once it is made; the caller releases it when it has read it
+  int plan = 0;
+  uint32_t plan_turn = 0;
+  auto next_plan = [&](const Plan*& p) {
+    if (!wait_warp(plan_full(plan), plan_turn)) return false;
+    p = plans + plan;
+    return uni(p->h) >= 0;
+  };
+  auto release_plan = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(plan_empty(plan));
+    if (++plan == kPlans) {
+      plan = 0;
+      plan_turn ^= 1;
+    }
+  };
 
-  if (warp == 9) {
-    // ---- TMA producer ----
-    if (lane == 0) {
-      int g = 0, nq[2] = {0, 0};
+  // (In the issuing roles, flags of the two tiles and the parities of their
+  // barriers are bits x of a word: the loops over x stay rolled.)
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == 9) {
+      // ---- TMA producer ----
+      const bool lead = elect_one() != 0;
+      int slot = 0;                        // of the ring
+      uint32_t turn = 1, loaded = 0;       // parity of an empty slot's wait; slots ever filled
+      uint32_t q_turn = 0, q_loaded = 0;   // bit x
       bool ok = true;
-      auto put = [&](const CUtensorMap* map, int row) {
-        const int s = g % NS;
-        if (g >= NS && !wait(kv_empty(s), ((g / NS) - 1) & 1)) return ok = false;
-        mbar_arrive_expect_tx(kv_full(s), SL::kBuf);
+      auto put = [&](const CUtensorMap* map, int h, int row) {
+        if (((loaded >> slot) & 1) && !wait_warp(kv_empty(slot), turn)) return ok = false;
+        loaded |= 1u << slot;
+        const uint32_t dst = sbase + SL::kKv + slot * SL::kBuf;
+        if (lead) {
+          mbar_arrive_expect_tx(kv_full(slot), SL::kBuf);
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(sbase + SL::kKv + s * SL::kBuf + c * SL::kBox, map, c * 64, it.h, row, kv_full(s));
-        ++g;
+          for (int c = 0; c < D / 64; ++c) tma_load_3d(dst + c * SL::kBox, map, c * 64, h, row, kv_full(slot));
+        }
+        if (++slot == NS) {
+          slot = 0;
+          turn ^= 1;
+        }
         return true;
       };
-      for (int item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
-        if (!it.load(a, item, end)) continue;
-        for (int c = 0; c < it.nc && ok; ++c) {
-          const int row = it.base(c);
-          if (!put(&tmk, row)) break;
+      const Plan* p;
+#pragma unroll 1
+      while (ok && next_plan(p)) {
+        const int h = uni(p->h);
+        const Chunks ch(a, *p);
+        const int q0[2] = {uni(p->t0), uni(p->t0 + p->count[0])};
+        const bool any1 = uni(p->count[1]) > 0;
+        release_plan();
+#pragma unroll 1
+        for (int c = 0; c < ch.nc && ok; ++c) {
+          const int row = ch.base(c);
+          if (!put(&tmk, h, row)) break;
           if (c == 0) {
-            for (int x = 0; x < 2 && ok; ++x) {
-              if (it.t1[x] == it.t0[x]) continue;
-              if (nq[x] > 0 && !wait(q_empty(x), (nq[x] - 1) & 1)) {
-                ok = false;
-                break;
-              }
-              mbar_arrive_expect_tx(q_full(x), a.tq * a.group * 128 * (D / 64));
 #pragma unroll
-              for (int k = 0; k < D / 64; ++k)
-                tma_load_3d(sbase + SL::kQ + x * SL::kBuf + k * SL::kBox, &tmq, k * 64, it.h * a.group,
-                            it.t0[x], q_full(x));
-              ++nq[x];
+            for (int x = 0; x < 2; ++x) {
+              if (!ok || (x == 1 && !any1)) continue;
+              if (((q_loaded >> x) & 1) && !(ok = wait_warp(q_empty(x), ((q_turn >> x) & 1) ^ 1))) continue;
+              if (lead) {
+                mbar_arrive_expect_tx(q_full(x), a.tq * a.group * 128 * (D / 64));
+#pragma unroll
+                for (int k = 0; k < D / 64; ++k)
+                  tma_load_3d(sbase + SL::kQ + x * SL::kBuf + k * SL::kBox, &tmq, k * 64, h * a.group, q0[x], q_full(x));
+              }
+              q_loaded |= 1u << x;
+              q_turn ^= 1u << x;
             }
             if (!ok) break;
           }
-          if (!put(&tmv, row)) break;
+          if (!put(&tmv, h, row)) break;
         }
       }
       // no copy into this CTA's shared memory may be in flight when it exits
       bool drained = true;
-      for (int k = g - 1; drained && k >= 0 && k >= g - NS; --k) drained = wait(kv_full(k % NS), (k / NS) & 1);
-      for (int x = 0; x < 2 && drained; ++x)
-        if (nq[x] > 0) drained = wait(q_full(x), (nq[x] - 1) & 1);
-    }
-  } else if (warp == 8) {
-    // ---- MMA issuer ----
-    if (lane == 0) {
-      constexpr uint32_t idesc_o = idesc_bf16_f32(kTile, D) | (1u << 16);     // B MN-major
-      int g = 0, nq[2] = {0, 0}, np[2] = {0, 0}, ns[2] = {0, 0}, no[2] = {0, 0};
-      // the previous chunk's P V still to be issued
-      bool todo[2] = {false, false}, opens[2] = {}, closes[2] = {};
-      int v_use = 0, v_steps = 0;
-      bool v_ready = false, ok = true;
-      auto product = [&](int x) {
-        if (!v_ready && !(ok = wait(kv_full(v_use % NS), (v_use / NS) & 1))) return;
-        v_ready = true;
-        if (!(ok = wait(p_full(x), np[x] & 1))) return;
-        ++np[x];
-        tc_fence_after();
-        const uint32_t v = sbase + SL::kKv + (v_use % NS) * SL::kBuf;
-        for (int k = 0; k < v_steps; ++k)
-          mma_ts(o_at(x), s_at(x) + k * 8, smem_desc_v(v + k * 16 * 128), idesc_o, !opens[x] || k > 0);
-        if (closes[x]) {
-          tc_commit<1>(o_full(x));
-          ++no[x];
+#pragma unroll 1
+      for (int k = 0; k < NS && drained; ++k) {
+        if (--slot < 0) {
+          slot = NS - 1;
+          turn ^= 1;
         }
-        todo[x] = false;
+        if ((loaded >> slot) & 1) drained = wait_warp(kv_full(slot), turn ^ 1);
+      }
+#pragma unroll 1
+      for (int x = 0; x < 2 && drained; ++x)
+        if ((q_loaded >> x) & 1) drained = wait_warp(q_full(x), ((q_turn >> x) & 1) ^ 1);
+    }
+    if (warp == 10) {
+      // ---- planner ----
+      const int end = a.offsets[a.n], pairs = a.items / a.hkv;
+      bool again = false, ok = true;       // a plan was in this place before
+      uint32_t turn = 1;
+      auto begin = [&]() { return !again || wait_warp(plan_empty(plan), turn); };
+      auto publish = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(plan_full(plan));
+        if (++plan == kPlans) {
+          plan = 0;
+          turn ^= 1;
+          again = true;
+        }
       };
+#pragma unroll 1
       for (int item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
-        if (!it.load(a, item, end)) continue;
-        bool fresh[2] = {true, true};
-        const int last[2] = {it.last(0), it.last(1)};
-        for (int c = 0; c < it.nc && ok; ++c) {
-          const int n16 = (it.keys(c) + 15) / 16;
-          const bool v_pending = todo[0] || todo[1];
-          const int v_slot = v_use % NS;
-          const bool sees[2] = {it.sees(0, c), it.sees(1, c)};
+        const int t0 = (pairs - 1 - item / a.hkv) * 2 * a.tq;
+        const int count = min(2 * a.tq, end - t0);
+        if (count <= 0) continue;
+        if (!(ok = begin())) break;
+        Plan& p = plans[plan];
+#pragma unroll 2
+        for (int i = lane; i < count; i += 32) {
+          const int t = t0 + i;
+          const int start = a.offsets[upper_index(a.offsets, a.n, t)];
+          p.begins[i] = static_cast<uint8_t>(max(0, start - t0));
+          if (i == 0 || i == a.tq) {
+            const int x = i == 0 ? 0 : 1;
+            p.start[x] = start;
+            p.lo[x] = a.window > 0 ? max(start, t - a.window + 1) : start;
+          }
+        }
+        if (lane == 0) {
+          p.h = item % a.hkv;
+          p.t0 = t0;
+          p.count[0] = min(count, a.tq);
+          p.count[1] = count - p.count[0];
+        }
+        publish();
+      }
+      if (ok && begin()) {
+        if (lane == 0) plans[plan].h = -1;
+        publish();
+      }
+    }
+    if (warp == 8) {
+      // ---- MMA issuer ----
+      const uint32_t lead = elect_one();
+      constexpr uint32_t idesc_o = idesc_bf16_f32(kTile, D) | (1u << 16);     // B MN-major
+      int slot = 0;                        // of the chunk's K; its V lies in the next one
+      uint32_t turn = 0;                   // parity of that slot's full barrier
+      uint32_t q_turn = 0, p_turn = 0, s_turn = 0, o_turn = 0;    // bit x
+      // the previous chunk's P V still to be issued, and its V
+      uint32_t todo = 0, opens = 0, closes = 0;
+      int v_slot = 0, v_steps = 0;
+      uint32_t v_turn = 0;
+      bool ok = true;
+      auto product = [&](int x) {
+        if (!(ok = wait_warp(p_full(x), (p_turn >> x) & 1))) return;
+        p_turn ^= 1u << x;
+        tc_fence_after();
+        const uint32_t d = o_at(x), p = s_at(x);
+        const uint64_t v = smem_desc_v(sbase + SL::kKv + v_slot * SL::kBuf);
+        const bool fresh = (opens >> x) & 1;
+        if (v_steps == kTile / 16) {
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)                     // 16 keys: 2048 bytes of V
+            mma_ts(lead, d, p + k * 8, v + 128ull * k, idesc_o, !fresh || k > 0);
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < v_steps; ++k) mma_ts(lead, d, p + k * 8, v + 128ull * k, idesc_o, !fresh || k > 0);
+        }
+        if ((closes >> x) & 1) {
+          commit(lead, o_full(x));
+          o_turn ^= 1u << x;
+        }
+      };
+      const Plan* p;
+#pragma unroll 1
+      while (ok && next_plan(p)) {
+        const Chunks ch(a, *p);
+        const Tile tile0(*p, 0), tile1(*p, 1);
+        release_plan();
+        const int last0 = tile0.last(ch), last1 = tile1.last(ch);
+        uint32_t fresh = 3;
+#pragma unroll 1
+        for (int c = 0; c < ch.nc && ok; ++c) {
+          const int kb = ch.base(c), kn = ch.keys(c);
+          const int n16 = (kn + 15) / 16;
+          const uint32_t sees = (tile0.sees(a, kb, kn) ? 1u : 0u) | (tile1.sees(a, kb, kn) ? 2u : 0u);
+          const uint32_t ends = (c == last0 ? 1u : 0u) | (c == last1 ? 2u : 0u);
+          const uint32_t idesc_s = idesc_bf16_f32(kTile, n16 * 16);
+          const uint64_t kd = smem_desc_k_sw128(sbase + SL::kKv + slot * SL::kBuf);
+          if (todo != 0 && !(ok = wait_warp(kv_full(v_slot), v_turn))) break;
           bool k_ready = false;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if (todo[x]) product(x);
-            if (!ok) break;
-            if (x == 1 && v_pending) tc_commit<1>(kv_empty(v_slot));
-            if (!sees[x]) continue;
-            if (fresh[x] && !(ok = wait(q_full(x), nq[x] & 1))) break;
-            if (!k_ready && !(ok = wait(kv_full(g % NS), (g / NS) & 1))) break;
+            if (!ok) continue;
+            if ((todo >> x) & 1) product(x);
+            if (!ok) continue;
+            if (x == 1 && todo != 0) commit(lead, kv_empty(v_slot));
+            if (!((sees >> x) & 1)) continue;
+            if (((fresh >> x) & 1) && !(ok = wait_warp(q_full(x), (q_turn >> x) & 1))) continue;
+            if (!k_ready && !(ok = wait_warp(kv_full(slot), turn))) continue;
             k_ready = true;
             tc_fence_after();
-            const uint32_t idesc_s = idesc_bf16_f32(kTile, n16 * 16);
-            const uint32_t q = sbase + SL::kQ + x * SL::kBuf, k = sbase + SL::kKv + (g % NS) * SL::kBuf;
+            const uint64_t qd = smem_desc_k_sw128(sbase + SL::kQ + x * SL::kBuf);
+            const uint32_t d = s_at(x);
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-              mma_ss(s_at(x), smem_desc_k_sw128(q + (ks / 4) * SL::kBox) + 2ull * (ks % 4),
-                     smem_desc_k_sw128(k + (ks / 4) * SL::kBox) + 2ull * (ks % 4), idesc_s, ks > 0);
-            tc_commit<1>(s_full(x));
-            ++ns[x];
-            if (c == last[x]) {
-              tc_commit<1>(q_empty(x));
-              ++nq[x];
+            for (int ks = 0; ks < D / 16; ++ks) {                   // 16 dims: 32 bytes of a box's rows
+              const uint64_t off = (ks / 4) * (SL::kBox / 16) + 2ull * (ks % 4);
+              mma_ss(lead, d, qd + off, kd + off, idesc_s, ks > 0);
+            }
+            commit(lead, s_full(x));
+            s_turn ^= 1u << x;
+            if ((ends >> x) & 1) {
+              commit(lead, q_empty(x));
+              q_turn ^= 1u << x;
             }
           }
           if (!ok) break;
-          tc_commit<1>(kv_empty(g % NS));
-          for (int x = 0; x < 2; ++x) {
-            todo[x] = sees[x];
-            opens[x] = fresh[x];
-            closes[x] = c == last[x];
-            if (sees[x]) fresh[x] = false;
-          }
-          v_use = g + 1;
+          commit(lead, kv_empty(slot));
+          todo = sees;
+          opens = fresh;
+          closes = ends;
+          fresh &= ~sees;
           v_steps = n16;
-          v_ready = false;
-          g += 2;
+          v_turn = turn;
+          if ((v_slot = slot + 1) == NS) {
+            v_slot = 0;
+            v_turn ^= 1;
+          }
+          turn = v_turn;
+          if ((slot = v_slot + 1) == NS) {
+            slot = 0;
+            turn ^= 1;
+          }
         }
       }
-      for (int x = 0; x < 2 && ok; ++x)
-        if (todo[x]) product(x);
-      // tensor memory is freed after the last MMAs have completed
+      if (ok && todo != 0) ok = wait_warp(kv_full(v_slot), v_turn);
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (ok && ((todo >> x) & 1)) product(x);
+      // tensor memory is freed after the last MMAs have completed (a barrier
+      // never used is in phase 0: the wait for parity 1 returns at once)
       bool drained = true;
-      for (int x = 0; x < 2 && drained; ++x) {
-        if (ns[x] > 0) drained = wait(s_full(x), (ns[x] - 1) & 1);
-        if (no[x] > 0 && drained) drained = wait(o_full(x), (no[x] - 1) & 1);
-      }
+#pragma unroll 1
+      for (int x = 0; x < 2 && drained; ++x)
+        drained = wait_warp(s_full(x), ((s_turn >> x) & 1) ^ 1) && wait_warp(o_full(x), ((o_turn >> x) & 1) ^ 1);
     }
   } else {
     // ---- softmax: one row per thread ----
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int x = warp >> 2;
-    const int row = (warp & 3) * 32 + lane;
     const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = s_at(x) + quarter, to = o_at(x) + quarter;
-    const int tok = row / a.group, head = row % a.group;
+    const int tok = ((warp & 3) * 32 + lane) / a.group;
     const uint64_t sc2 = f32x2_splat(a.scale_log2);
-    int ns = 0, no = 0;
+    uint32_t s_turn = 0, o_turn = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
-      if (!it.load(a, item, end)) continue;
-      if (it.t1[x] == it.t0[x]) continue;
-      const int t = it.t0[x] + tok;
-      const bool mine = tok < a.tq && t < it.t1[x];
-      Row r = {0, 0};
-      if (mine) r = row_of(a, t);
-      const int sink_end = mine ? min(r.start + min(a.sinks, r.lo - r.start), r.lo) : 0;
+    const Plan* p;
+#pragma unroll 1
+    while (ok && next_plan(p)) {
+      const int h = uni(p->h);
+      const Chunks ch(a, *p);
+      const Tile tile(*p, x);
+      const int t = tile.t0 + tok;
+      const bool mine = tok < a.tq && t < tile.t1;
+      int start = 0, lo = 0, sink_end = 0;    // of the row's keys
+      if (mine) {
+        const int b = p->begins[t - p->t0];
+        start = b == 0 ? ch.start : p->t0 + b;
+        lo = a.window > 0 ? max(start, t - a.window + 1) : start;
+        sink_end = start + min(a.sinks, lo - start);
+      }
+      release_plan();
+      if (tile.t1 == tile.t0) continue;
       // keys that every row of the warp admits: [all_lo, all_hi]
-      const int all_lo = __reduce_max_sync(0xffffffffu, mine ? r.lo : 0);
+      const int all_lo = __reduce_max_sync(0xffffffffu, lo);
       const int all_hi = __reduce_min_sync(0xffffffffu, mine ? t : 0x7fffffff);
       const bool any = __any_sync(0xffffffffu, mine);
       float ref = -INFINITY;             // base-2 reference of the row's exponentials
       uint64_t l2 = 0ull;
       bool begun = false;
-      for (int c = 0; c < it.nc; ++c) {
-        if (!it.sees(x, c)) continue;
-        const int kb = it.base(c), kn = it.keys(c);
-        if (!wait(s_full(x), ns & 1)) {
-          ok = false;
-          break;
-        }
-        ++ns;
-        tc_fence_after();
-        const bool full = kn == kTile && kb >= all_lo && kb + kTile - 1 <= all_hi && any;
-        uint32_t s[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (q * 32 < kn) tmem_ld_32cols(ts + q * 32, s[q]);
-        tmem_wait_ld();
-        if (!full) {
-          // masked scores become -inf
+#pragma unroll 1
+      for (int c = 0; c < ch.nc; ++c) {
+        const int kb = ch.base(c), kn = ch.keys(c);
+        if (!tile.sees(a, kb, kn)) continue;
+        // columns that the row admits, and the 32-key groups that some and
+        // that every row of the warp admits
+        uint32_t in[4];
+        uint32_t some = 0xfu, every = 0xfu;
+        if (!(kn == kTile && kb >= all_lo && kb + kTile - 1 <= all_hi && any)) {
+          some = every = 0;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int b = kb + q * 32;
-            const uint32_t in = !mine ? 0u
-                : low_bits(kn - q * 32) & ((low_bits(t + 1 - b) & ~low_bits(r.lo - b)) |
-                                           (low_bits(sink_end - b) & ~low_bits(r.start - b)));
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!(in & (1u << i))) s[q][i] = 0xff800000u;
+            in[q] = !mine ? 0u
+                : low_bits(kn - q * 32) & ((low_bits(t + 1 - b) & ~low_bits(lo - b)) |
+                                           (low_bits(sink_end - b) & ~low_bits(start - b)));
+            if (__any_sync(0xffffffffu, in[q] != 0u)) some |= 1u << q;
+            if (__all_sync(0xffffffffu, in[q] == 0xffffffffu || !mine)) every |= 1u << q;
           }
         }
-        float top = -INFINITY;
+        if (!wait_warp(s_full(x), s_turn)) {
+          ok = false;
+          break;
+        }
+        s_turn ^= 1;
+        tc_fence_after();
+        // S of 32-key group q; masked scores are -inf
+        auto load = [&](int q, uint32_t (&s)[32]) { tmem_ld_32cols(ts + q * 32, s); };
+        auto mask = [&](int q, uint32_t (&s)[32]) {
+          if ((every >> q) & 1) return;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            top = fmaxf(top, fmaxf(__uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1])));
-        top *= a.scale_log2;
-        const bool move = mine && top > ref + 8.f;
-        if (__any_sync(0xffffffffu, move)) {
-          const float now = move ? top : ref;
-          const float keep = ref == -INFINITY ? 0.f : ex2_approx_ftz(ref - now);
-          const float keep1 = move ? keep : 1.f;
-          ref = now;
-          const uint64_t k2 = f32x2_splat(keep1);
-          l2 = f32x2_mul(l2, k2);
-          if (begun) {
-            // the earlier chunks' products are complete: S of this chunk was
-            // issued behind them
-#pragma unroll
-            for (int q = 0; q < D / 16; ++q) {
-              uint32_t o[16];
-              tmem_ld_16cols(to + q * 16, o);
+          for (int i = 0; i < 32; ++i)
+            if (!(in[q] & (1u << i))) s[i] = 0xff800000u;
+        };
+        // 0: the reference stands; 1: rows without one take the maximum of
+        // the first keys they admit; 2: the maximum of all
+        int look = __any_sync(0xffffffffu, mine && ref == -INFINITY) ? 1 : 0;
+        uint32_t pk[4][16];
+        uint64_t add2;
+        for (;;) {
+          if (look != 0) {
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              if (!((some >> q) & 1)) continue;
+              uint32_t s[32];
+              load(q, s);
               tmem_wait_ld();
+              const uint32_t iq = (every >> q) & 1 ? 0xffffffffu : (q < 2 ? (q == 0 ? in[0] : in[1]) : (q == 2 ? in[2] : in[3]));
+              float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep1);
-              tmem_st_16cols(to + q * 16, o);
+              for (int i = 0; i < 32; ++i)
+                if (iq & (1u << i)) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(s[i]));
+              top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+              if (look == 1 && __all_sync(0xffffffffu, !mine || top > -INFINITY || ref > -INFINITY)) break;
+            }
+            top *= a.scale_log2;
+            const bool move = mine && top > ref + 8.f;
+            if (__any_sync(0xffffffffu, move)) {
+              const float now = move ? top : ref;
+              const float keep = !move ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx_ftz(ref - now));
+              ref = now;
+              l2 = f32x2_mul(l2, f32x2_splat(keep));
+              if (begun) {
+                // the earlier chunks' products are complete: S of this chunk
+                // was issued behind them
+#pragma unroll 1
+                for (int q = 0; q < D / 16; ++q) {
+                  uint32_t o[16];
+                  tmem_ld_16cols(to + q * 16, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                  tmem_st_16cols(to + q * 16, o);
+                }
+              }
             }
           }
+          // P against the reference as it stands, and the maximum beside it
+          const uint64_t neg = f32x2_splat(ref == -INFINITY ? 0.f : -ref);
+          float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
+          uint32_t s[4][32];
+          auto group = [&](int q) {
+            if (!((some >> q) & 1)) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) pk[q][i] = 0u;
+              return;
+            }
+            mask(q, s[q]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float s0 = __uint_as_float(s[q][2 * i]), s1 = __uint_as_float(s[q][2 * i + 1]);
+              top4[i & 3] = fmaxf(top4[i & 3], fmaxf(s0, s1));
+              float x0, x1;
+              f32x2_unpack(f32x2_fma(f32x2_pack(s0, s1), sc2, neg), x0, x1);
+              const float p0 = ex2_approx_ftz(x0), p1 = ex2_approx_ftz(x1);
+              sum4[i & 3] = f32x2_add(sum4[i & 3], f32x2_pack(p0, p1));
+              pk[q][i] = pack_bf16x2(p0, p1);
+            }
+          };
+          // 64 keys are on their way while 64 are worked on
+          load(0, s[0]);
+          load(1, s[1]);
+          tmem_wait_ld();
+          if (some >> 2) {
+            load(2, s[2]);
+            load(3, s[3]);
+          }
+          group(0);
+          group(1);
+          if (some >> 2) tmem_wait_ld();
+          group(2);
+          group(3);
+          const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+          add2 = f32x2_add(f32x2_add(sum4[0], sum4[1]), f32x2_add(sum4[2], sum4[3]));
+          if (!__any_sync(0xffffffffu, mine && top * a.scale_log2 > ref + 8.f)) break;
+          look = 2;
         }
         begun = true;
-        const uint64_t neg = f32x2_splat(ref == -INFINITY ? 0.f : -ref);
+        l2 = f32x2_add(l2, add2);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (q * 32 >= kn) continue;
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x0, x1;
-            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), sc2, neg),
-                         x0, x1);
-            const float p0 = ex2_approx_ftz(x0), p1 = ex2_approx_ftz(x1);
-            l2 = f32x2_add(l2, f32x2_pack(p0, p1));
-            pk[i] = pack_bf16x2(p0, p1);
-          }
-          tmem_st_16cols(ts + q * 16, pk);
-        }
+        for (int q = 0; q < 4; ++q)
+          if (q * 32 < kn) tmem_st_16cols(ts + q * 16, pk[q]);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(x));
       }
-      if (!ok || !wait(o_full(x), no & 1)) {
+      if (!ok || !wait_warp(o_full(x), o_turn)) {
         ok = false;
         break;
       }
-      ++no;
+      o_turn ^= 1;
       tc_fence_after();
       float l0, l1;
       f32x2_unpack(l2, l0, l1);
       const float inv = 1.f / (l0 + l1);
-      bf16* dst = a.out + t * a.out_stride + static_cast<int64_t>(it.h * a.group + head) * D;
+      const int head = h * a.group + ((warp & 3) * 32 + lane) % a.group;
+      bf16* dst = a.out + t * a.out_stride + static_cast<int64_t>(head) * D;
       bool fine = true;
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {
@@ -462,22 +661,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_32cols(to + q * 32, o);
         tmem_wait_ld();
         float worst = 0.f;
+        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float y = __uint_as_float(o[i]) * inv;
-          worst = fmaf(y, 0.f, worst);               // NaN once y is not finite
-          o[i] = __float_as_uint(y);
+        for (int i = 0; i < 16; ++i) {
+          const float y0 = __uint_as_float(o[2 * i]) * inv, y1 = __uint_as_float(o[2 * i + 1]) * inv;
+          worst = fmaf(y0, 0.f, fmaf(y1, 0.f, worst));      // NaN once one is not finite
+          w[i] = pack_bf16x2(y0, y1);
         }
         fine = fine && worst == 0.f;
         if (mine) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]), __uint_as_float(o[8 * i + 2 * e + 1]));
-            reinterpret_cast<uint4*>(dst)[q * 4 + i] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4*>(dst)[q * 4 + i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
         }
       }
       tc_fence_before();
@@ -485,13 +680,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (odd != 0) {
         // does a V row that some row of the tile does not see hold the cause?
         bool cause = false;
-        for (int c = 0; c < it.nc; ++c) {
-          const int kb = it.base(c), kn = it.keys(c);
-          if (!it.sees(x, c) || (kb >= all_lo && kb + kn - 1 <= all_hi)) continue;
-          const int rows = min(kTile, ((kn + 15) / 16) * 16);
+        for (int c = 0; c < ch.nc; ++c) {
+          const int kb = ch.base(c), kn = ch.keys(c);
+          if (!tile.sees(a, kb, kn) || (kb >= all_lo && kb + kn - 1 <= all_hi)) continue;
+          const int rows = min(((kn + 15) / 16) * 16, a.tmax - kb);      // what the products read
           for (int j = lane; j < rows; j += 32) {
-            if (kb + j >= a.tmax) continue;
-            const bf16* vr = a.v + (kb + j) * a.v_stride + it.h * D;
+            const bf16* vr = a.v + (kb + j) * a.v_stride + h * D;
             for (int e = 0; e < D / 8; ++e) {
               float f[8];
               Chunk8<bf16>::load(vr + 8 * e, f);
@@ -504,22 +698,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (uint32_t left = odd; left != 0; left &= left - 1) {
             const int src = __ffs(left) - 1;
             const int64_t tt = __shfl_sync(0xffffffffu, t, src);
-            const int hh = it.h * a.group + __shfl_sync(0xffffffffu, head, src);
-            const int st = __shfl_sync(0xffffffffu, r.start, src), lo = __shfl_sync(0xffffffffu, r.lo, src);
+            const int64_t hh = __shfl_sync(0xffffffffu, head, src);
+            const int st = __shfl_sync(0xffffffffu, start, src), from = __shfl_sync(0xffffffffu, lo, src);
             const int se = __shfl_sync(0xffffffffu, sink_end, src);
             auto ptr = [&](int64_t j, const bf16*& kp, const bf16*& vp) {
-              kp = a.k + j * a.k_stride + it.h * D;
-              vp = a.v + j * a.v_stride + it.h * D;
+              kp = a.k + j * a.k_stride + h * D;
+              vp = a.v + j * a.v_stride + h * D;
             };
-            const bf16* q = a.q + tt * a.q_stride + static_cast<int64_t>(hh) * D;
+            const bf16* q = a.q + tt * a.q_stride + hh * D;
             RowState<D> state;
             attend_keys<D>(q, a.scale_log2, st, se, ptr, state);
-            attend_keys<D>(q, a.scale_log2, lo, tt + 1, ptr, state);
+            attend_keys<D>(q, a.scale_log2, from, tt + 1, ptr, state);
             const float il = 1.f / state.l;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i)
-              a.out[tt * a.out_stride + static_cast<int64_t>(hh) * D + lane + 32 * i] =
-                  __float2bfloat16_rn(state.o[i] * il);
+              a.out[tt * a.out_stride + hh * D + lane + 32 * i] = __float2bfloat16_rn(state.o[i] * il);
           }
         }
       }
