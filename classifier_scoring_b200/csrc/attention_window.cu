@@ -25,12 +25,12 @@
 //             (the tensor pipe runs its MMAs in order).  While one tile's
 //             softmax runs, the other tile's MMAs do.  K chunks of fewer keys
 //             take fewer columns; chunks that a tile does not see are skipped;
-//   warps 0..7 : softmax, four warps a tile, one row per thread, 64 keys at a
-//             time: the exponentials with the scale folded into one packed FMA,
+//   warps 0..7 : softmax, four warps a tile, one row per thread: the
+//             row of S in registers, the exponentials with the scale folded into one packed FMA,
 //             against a reference that follows the row's maximum only when that
 //             is 2^8 ahead (then O is rescaled in tensor memory by the same
-//             thread), so that no exponential waits for a maximum; P as bf16
-//             back to tensor memory.  32-key groups that every row of a warp
+//             thread); P as bf16 back to tensor memory, where the products of
+//             the first 64 keys begin while the others are worked on.  32-key groups that every row of a warp
 //             admits take no masks, those that none admits are skipped.  After
 //             the last chunk the thread reads its row of O, divides, stores.
 // Tensor memory: S_0, S_1 (P over them), O_0, O_1: 512 columns for d = 128.
@@ -76,13 +76,14 @@ struct Plan {
 template <int D> struct Smem {
   static constexpr int kBox = kTile * 128;                 // 64 dims of 128 rows
   static constexpr int kBuf = kBox * (D / 64);             // a Q tile, K chunk or V chunk
-  static constexpr int kSlots = D == 128 ? 5 : 10;
+  static constexpr int kSlots = D == 128 ? 4 : 8;          // two chunks, or four
   static constexpr int kQ = 0;
   static constexpr int kKv = 2 * kBuf;
-  static constexpr int kBar = kKv + kSlots * kBuf;
-  // q_full[2] q_empty[2] s_full[2] p_full[2] o_full[2] plan_full[] plan_empty[]
-  // kv_full[] kv_empty[]
-  static constexpr int kBars = 10 + 2 * kPlans + 2 * kSlots;
+  static constexpr int kOut = kKv + kSlots * kBuf;         // 64 dims of each tile's output rows
+  static constexpr int kBar = kOut + 2 * kBox;
+  // q_full[2] q_empty[2] s_full[2] o_full[2] p_full[2][2] plan_full[]
+  // plan_empty[] kv_full[] kv_empty[]
+  static constexpr int kBars = 12 + 2 * kPlans + 2 * kSlots;
   static constexpr int kTmemSlot = kBar + kBars * 8;
   static constexpr int kPlan = kTmemSlot + 16;
   static constexpr int kBytes = kPlan + kPlans * static_cast<int>(sizeof(Plan)) + 1024;   // + alignment slack
@@ -155,6 +156,23 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait(bar, parity));
 }
 
+// Barriers of the 128 threads of tile x's softmax; tile_all also ANDs a flag.
+__device__ __forceinline__ void tile_sync(int x) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
+}
+__device__ __forceinline__ bool tile_all(int x, bool flag) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"(flag ? 1u : 0u), "r"(1 + x)
+      : "memory");
+  return r != 0;
+}
+
 // An item's key chunks.  Chunks 0..nsc-1 cover the sinks [start, start +
 // nsink) of the first token's sequence that lie before the window of every
 // row; the others [lo, hi).
@@ -190,7 +208,8 @@ struct Tile {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_window_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                       const __grid_constant__ CUtensorMap tmv, const WindowArgs a) {
+                       const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo,
+                       const WindowArgs a) {
   using SL = Smem<D>;
   constexpr int NS = SL::kSlots;
   extern __shared__ uint8_t raw[];
@@ -201,12 +220,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto q_full = [&](int x) { return bar0 + 8u * x; };
   auto q_empty = [&](int x) { return bar0 + 8u * (2 + x); };
   auto s_full = [&](int x) { return bar0 + 8u * (4 + x); };
-  auto p_full = [&](int x) { return bar0 + 8u * (6 + x); };
-  auto o_full = [&](int x) { return bar0 + 8u * (8 + x); };
-  auto plan_full = [&](int e) { return bar0 + 8u * (10 + e); };
-  auto plan_empty = [&](int e) { return bar0 + 8u * (10 + kPlans + e); };
-  auto kv_full = [&](int s) { return bar0 + 8u * (10 + 2 * kPlans + s); };
-  auto kv_empty = [&](int s) { return bar0 + 8u * (10 + 2 * kPlans + NS + s); };
+  auto o_full = [&](int x) { return bar0 + 8u * (6 + x); };
+  auto p_full = [&](int x, int half) { return bar0 + 8u * (8 + 2 * x + half); };
+  auto plan_full = [&](int e) { return bar0 + 8u * (12 + e); };
+  auto plan_empty = [&](int e) { return bar0 + 8u * (12 + kPlans + e); };
+  auto kv_full = [&](int s) { return bar0 + 8u * (12 + 2 * kPlans + s); };
+  auto kv_empty = [&](int s) { return bar0 + 8u * (12 + 2 * kPlans + NS + s); };
   Plan* plans = reinterpret_cast<Plan*>(sm + SL::kPlan);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + SL::kTmemSlot);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -216,7 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(q_full(x), 1);
       mbar_init(q_empty(x), 1);
       mbar_init(s_full(x), 1);
-      mbar_init(p_full(x), 4);           // the tile's four warps
+      mbar_init(p_full(x, 0), 4);        // the tile's four warps
+      mbar_init(p_full(x, 1), 4);
       mbar_init(o_full(x), 1);
     }
     for (int e = 0; e < kPlans; ++e) {
@@ -388,19 +408,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t v_turn = 0;
       bool ok = true;
       auto product = [&](int x) {
-        if (!(ok = wait_warp(p_full(x), (p_turn >> x) & 1))) return;
-        p_turn ^= 1u << x;
-        tc_fence_after();
         const uint32_t d = o_at(x), p = s_at(x);
         const uint64_t v = smem_desc_v(sbase + SL::kKv + v_slot * SL::kBuf);
         const bool fresh = (opens >> x) & 1;
-        if (v_steps == kTile / 16) {
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)                     // 16 keys: 2048 bytes of V
-            mma_ts(lead, d, p + k * 8, v + 128ull * k, idesc_o, !fresh || k > 0);
-        } else {
+        for (int half = 0; half < 2; ++half) {                     // P comes 64 keys at a time
+          if (v_steps <= half * 4) continue;
+          if (!(ok = wait_warp(p_full(x, half), (p_turn >> (2 * x + half)) & 1))) return;
+          p_turn ^= 1u << (2 * x + half);
+          tc_fence_after();
+          if (v_steps >= half * 4 + 4) {
+#pragma unroll
+            for (int k = half * 4; k < half * 4 + 4; ++k)          // 16 keys: 2048 bytes of V
+              mma_ts(lead, d, p + k * 8, v + 128ull * k, idesc_o, !fresh || k > 0);
+          } else {
 #pragma unroll 1
-          for (int k = 0; k < v_steps; ++k) mma_ts(lead, d, p + k * 8, v + 128ull * k, idesc_o, !fresh || k > 0);
+            for (int k = half * 4; k < v_steps; ++k) mma_ts(lead, d, p + k * 8, v + 128ull * k, idesc_o, !fresh || k > 0);
+          }
         }
         if ((closes >> x) & 1) {
           commit(lead, o_full(x));
@@ -491,8 +515,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t s_turn = 0, o_turn = 0;
     bool ok = true;
     const Plan* p;
+    // the tile's four warps take and leave an item together, a wait that gave
+    // up included: none is left at a barrier
 #pragma unroll 1
-    while (ok && next_plan(p)) {
+    while (tile_all(x, next_plan(p))) {
       const int h = uni(p->h);
       const Chunks ch(a, *p);
       const Tile tile(*p, x);
@@ -540,144 +566,140 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         s_turn ^= 1;
         tc_fence_after();
-        // S of 32-key group q; masked scores are -inf
-        auto load = [&](int q, uint32_t (&s)[32]) { tmem_ld_32cols(ts + q * 32, s); };
-        auto mask = [&](int q, uint32_t (&s)[32]) {
-          if ((every >> q) & 1) return;
+        // the row's scores; masked ones become -inf
+        uint32_t s[4][32];
+        tmem_ld_32cols(ts, s[0]);
+        tmem_ld_32cols(ts + 32, s[1]);
+        if (kn > 64) {
+          tmem_ld_32cols(ts + 64, s[2]);
+          tmem_ld_32cols(ts + 96, s[3]);
+        }
+        tmem_wait_ld();
+        float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!(in[q] & (1u << i))) s[i] = 0xff800000u;
-        };
-        // 0: the reference stands; 1: rows without one take the maximum of
-        // the first keys they admit; 2: the maximum of all
-        int look = __any_sync(0xffffffffu, mine && ref == -INFINITY) ? 1 : 0;
-        uint32_t pk[4][16];
-        uint64_t add2;
-        for (;;) {
-          if (look != 0) {
-            float top = -INFINITY;
+        for (int q = 0; q < 4; ++q) {
+          if (!((some >> q) & 1)) continue;
+          if (!((every >> q) & 1)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!(in[q] & (1u << i))) s[q][i] = 0xff800000u;
+          }
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            top4[(i / 2) & 3] = fmaxf(fmaxf(top4[(i / 2) & 3], __uint_as_float(s[q][i])), __uint_as_float(s[q][i + 1]));
+        }
+        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * a.scale_log2;
+        const bool move = mine && top > ref + 8.f;
+        if (__any_sync(0xffffffffu, move)) {
+          const float now = move ? top : ref;
+          const float keep = !move ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx_ftz(ref - now));
+          ref = now;
+          l2 = f32x2_mul(l2, f32x2_splat(keep));
+          if (begun) {
+            // the earlier chunks' products are complete: S of this chunk was
+            // issued behind them
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              if (!((some >> q) & 1)) continue;
-              uint32_t s[32];
-              load(q, s);
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              tmem_ld_16cols(to + q * 16, o);
               tmem_wait_ld();
-              const uint32_t iq = (every >> q) & 1 ? 0xffffffffu : (q < 2 ? (q == 0 ? in[0] : in[1]) : (q == 2 ? in[2] : in[3]));
-              float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (iq & (1u << i)) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(s[i]));
-              top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-              if (look == 1 && __all_sync(0xffffffffu, !mine || top > -INFINITY || ref > -INFINITY)) break;
-            }
-            top *= a.scale_log2;
-            const bool move = mine && top > ref + 8.f;
-            if (__any_sync(0xffffffffu, move)) {
-              const float now = move ? top : ref;
-              const float keep = !move ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx_ftz(ref - now));
-              ref = now;
-              l2 = f32x2_mul(l2, f32x2_splat(keep));
-              if (begun) {
-                // the earlier chunks' products are complete: S of this chunk
-                // was issued behind them
-#pragma unroll 1
-                for (int q = 0; q < D / 16; ++q) {
-                  uint32_t o[16];
-                  tmem_ld_16cols(to + q * 16, o);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                  tmem_st_16cols(to + q * 16, o);
-                }
-              }
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+              tmem_st_16cols(to + q * 16, o);
             }
           }
-          // P against the reference as it stands, and the maximum beside it
-          const uint64_t neg = f32x2_splat(ref == -INFINITY ? 0.f : -ref);
-          float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
-          uint32_t s[4][32];
-          auto group = [&](int q) {
-            if (!((some >> q) & 1)) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) pk[q][i] = 0u;
-              return;
-            }
-            mask(q, s[q]);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float s0 = __uint_as_float(s[q][2 * i]), s1 = __uint_as_float(s[q][2 * i + 1]);
-              top4[i & 3] = fmaxf(top4[i & 3], fmaxf(s0, s1));
-              float x0, x1;
-              f32x2_unpack(f32x2_fma(f32x2_pack(s0, s1), sc2, neg), x0, x1);
-              const float p0 = ex2_approx_ftz(x0), p1 = ex2_approx_ftz(x1);
-              sum4[i & 3] = f32x2_add(sum4[i & 3], f32x2_pack(p0, p1));
-              pk[q][i] = pack_bf16x2(p0, p1);
-            }
-          };
-          // 64 keys are on their way while 64 are worked on
-          load(0, s[0]);
-          load(1, s[1]);
-          tmem_wait_ld();
-          if (some >> 2) {
-            load(2, s[2]);
-            load(3, s[3]);
-          }
-          group(0);
-          group(1);
-          if (some >> 2) tmem_wait_ld();
-          group(2);
-          group(3);
-          const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-          add2 = f32x2_add(f32x2_add(sum4[0], sum4[1]), f32x2_add(sum4[2], sum4[3]));
-          if (!__any_sync(0xffffffffu, mine && top * a.scale_log2 > ref + 8.f)) break;
-          look = 2;
         }
         begun = true;
-        l2 = f32x2_add(l2, add2);
+        const uint64_t neg = f32x2_splat(ref == -INFINITY ? 0.f : -ref);
+        uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (q * 32 < kn) tmem_st_16cols(ts + q * 16, pk[q]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(x));
+        for (int half = 0; half < 2; ++half) {
+          if (kn <= half * 64) continue;
+#pragma unroll
+          for (int q = 2 * half; q < 2 * half + 2; ++q) {
+            uint32_t pk[16];
+            if ((some >> q) & 1) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float x0, x1;
+                f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), sc2, neg),
+                             x0, x1);
+                const float p0 = ex2_approx_ftz(x0), p1 = ex2_approx_ftz(x1);
+                sum4[i & 3] = f32x2_add(sum4[i & 3], f32x2_pack(p0, p1));
+                pk[i] = pack_bf16x2(p0, p1);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) pk[i] = 0u;
+            }
+            tmem_st_16cols(ts + q * 16, pk);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(x, half));
+        }
+        l2 = f32x2_add(l2, f32x2_add(f32x2_add(sum4[0], sum4[1]), f32x2_add(sum4[2], sum4[3])));
       }
-      if (!ok || !wait_warp(o_full(x), o_turn)) {
-        ok = false;
-        break;
-      }
+      if (ok) ok = wait_warp(o_full(x), o_turn);
+      if (!tile_all(x, ok)) break;
       o_turn ^= 1;
       tc_fence_after();
       float l0, l1;
       f32x2_unpack(l2, l0, l1);
       const float inv = 1.f / (l0 + l1);
       const int head = h * a.group + ((warp & 3) * 32 + lane) % a.group;
-      bf16* dst = a.out + t * a.out_stride + static_cast<int64_t>(head) * D;
-      bool fine = true;
+      uint32_t w[D / 2];
+      float worst = 0.f;
 #pragma unroll
-      for (int q = 0; q < D / 32; ++q) {
-        uint32_t o[32];
-        tmem_ld_32cols(to + q * 32, o);
+      for (int q = 0; q < D / 64; ++q) {
+        uint32_t o[2][32];
+        tmem_ld_32cols(to + q * 64, o[0]);
+        tmem_ld_32cols(to + q * 64 + 32, o[1]);
         tmem_wait_ld();
-        float worst = 0.f;
-        uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float y0 = __uint_as_float(o[2 * i]) * inv, y1 = __uint_as_float(o[2 * i + 1]) * inv;
+        for (int i = 0; i < 32; ++i) {
+          const float y0 = __uint_as_float(o[i >> 4][(2 * i) & 31]) * inv, y1 = __uint_as_float(o[i >> 4][(2 * i + 1) & 31]) * inv;
           worst = fmaf(y0, 0.f, fmaf(y1, 0.f, worst));      // NaN once one is not finite
-          w[i] = pack_bf16x2(y0, y1);
-        }
-        fine = fine && worst == 0.f;
-        if (mine) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            reinterpret_cast<uint4*>(dst)[q * 4 + i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          w[q * 32 + i] = pack_bf16x2(y0, y1);
         }
       }
       tc_fence_before();
+      const bool fine = worst == 0.f;
       const uint32_t odd = __ballot_sync(0xffffffffu, mine && !fine);
+      // A whole tile of finite rows leaves through shared memory, 64 dims at a
+      // time, as one box (row by row, a warp's store would touch 32 lines);
+      // other tiles row by row.  (bar.red: the tile's four warps agree.)
+      const bool box = tile_all(x, odd == 0) && tile.t1 - tile.t0 == a.tq;
+      if (box) {
+        const int r = (warp & 3) * 32 + lane;
+        const uint32_t out = sbase + SL::kOut + x * SL::kBox;
+#pragma unroll
+        for (int q = 0; q < D / 64; ++q) {
+          // the previous box has been read out of shared memory
+          if (r == 0) bulk_wait_group_read<0>();
+          tile_sync(x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + r * 128 + ((i ^ (r & 7)) << 4)),
+                         "r"(w[q * 32 + 4 * i]), "r"(w[q * 32 + 4 * i + 1]), "r"(w[q * 32 + 4 * i + 2]),
+                         "r"(w[q * 32 + 4 * i + 3])
+                         : "memory");
+          fence_proxy_async_smem();
+          tile_sync(x);
+          if (r == 0) {
+            tma_store_3d(&tmo, out, q * 64, h * a.group, tile.t0);
+            bulk_commit_group();
+          }
+        }
+      } else if (mine) {
+        bf16* dst = a.out + t * a.out_stride + static_cast<int64_t>(head) * D;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      }
       if (odd != 0) {
+        __syncwarp();                           // the rows are written before they are written again
         // does a V row that some row of the tile does not see hold the cause?
         bool cause = false;
         for (int c = 0; c < ch.nc; ++c) {
@@ -718,6 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+  if (warp < 8) bulk_wait_group<0>();      // the boxes are written before shared memory goes
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -729,17 +752,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D>
 cudaError_t launch(const WindowArgs& a, int T, int grid, cudaStream_t st) {
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, to;
   const char* why = "";
   if (!make_tmap_heads(&tq, a.q, T, a.hq, D, a.q_stride, a.group, a.tq, &why) ||
       !make_tmap_heads(&tk, a.k, T, a.hkv, D, a.k_stride, 1, kTile, &why) ||
-      !make_tmap_heads(&tv, a.v, T, a.hkv, D, a.v_stride, 1, kTile, &why))
+      !make_tmap_heads(&tv, a.v, T, a.hkv, D, a.v_stride, 1, kTile, &why) ||
+      !make_tmap_heads(&to, a.out, T, a.hq, D, a.out_stride, a.group, a.tq, &why))
     return cudaErrorInvalidValue;
   auto kernel = attn_window_kernel<D>;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, Smem<D>::kBytes, st>>>(tq, tk, tv, a);
+  kernel<<<grid, kThreads, Smem<D>::kBytes, st>>>(tq, tk, tv, to, a);
   return cudaGetLastError();
 }
 
