@@ -15,24 +15,35 @@
 // the item's keys are one range of packed rows, plus the first sequence's
 // sinks when its window has left them behind.  Items are dealt to one
 // persistent CTA per SM, the last tokens (which see most) first:
-//   warp 10 : plans items ahead of the others: key range, chunks and the start of
+//   warp 19 : plans items ahead of the others: key range, chunks and the start of
 //             each row's sequence (searches in the offsets) into shared memory;
-//   warp 9  : TMA -- the two Q tiles of an item and, per 128-key chunk, K and V
+//   warp 18 : TMA -- the two Q tiles of an item and, per 128-key chunk, K and V
 //             through a ring of slots (128-byte swizzle, rows past the batch
 //             read as zeros);
-//   warp 8  : tcgen05.mma, per chunk and tile X: O_X += P_X V of the previous
-//             chunk, then S_X = Q_X K^T into the columns that P_X just left
-//             (the tensor pipe runs its MMAs in order).  While one tile's
-//             softmax runs, the other tile's MMAs do.  K chunks of fewer keys
+//   warps 16, 17 : tcgen05.mma, a warp a tile, per chunk: O_X += P_X V of the
+//             previous chunk, then S_X = Q_X K^T into the columns that P_X just
+//             left (a warp's MMAs run in order).  While one tile's softmax
+//             runs, the other tile's MMAs do: the warps take turns at the
+//             tensor pipe, a chunk's MMAs of one tile at a time (interleaved,
+//             both tiles' scores would be ready at the same time, and the
+//             softmax and the MMAs would wait for each other).  One warp for
+//             both tiles spent longer on its waits and descriptors than the
+//             MMAs take.  K chunks of fewer keys
 //             take fewer columns; chunks that a tile does not see are skipped;
-//   warps 0..7 : softmax, four warps a tile, one row per thread: the
-//             row of S in registers, the exponentials with the scale folded into one packed FMA,
-//             against a reference that follows the row's maximum only when that
-//             is 2^8 ahead (then O is rescaled in tensor memory by the same
-//             thread); P as bf16 back to tensor memory, where the products of
-//             the first 64 keys begin while the others are worked on.  32-key groups that every row of a warp
-//             admits take no masks, those that none admits are skipped.  After
-//             the last chunk the thread reads its row of O, divides, stores.
+//   warps 0..15 : softmax, eight warps a tile: a row belongs to two threads, one
+//             for each 64 keys of a chunk (twice the warps for the latencies of
+//             tensor memory and of the special-function unit to hide behind,
+//             and half the code in each).  They read their scores, take the
+//             exponentials with the scale folded into one packed FMA, and write
+//             P as bf16 back to tensor memory.  The reference of the
+//             exponentials is the row's maximum over its first chunk and
+//             follows it only when a later one is 2^8 ahead: then the row's
+//             threads meet over the new maximum, rescale O (in tensor memory,
+//             each half the dims) and take the chunk again, so that otherwise
+//             no exponential waits for a maximum.  32-key groups that every row of a
+//             warp admits take no masks, those that none admits are skipped.
+//             After the last chunk each thread reads half the dims of its row
+//             of O, divides and stores.
 // Tensor memory: S_0, S_1 (P over them), O_0, O_1: 512 columns for d = 128.
 //
 // A masked key has P = 0, but 0 times an infinity or NaN in its V row would
@@ -56,11 +67,9 @@ namespace {
 __device__ int32_t g_window_err[ERR_WORDS];
 
 constexpr int kTile = 128;              // rows of a tile, keys of a chunk
-constexpr int kThreads = 384;           // 8 softmax warps; MMA, TMA and two idle ones
-// registers of the two kinds of warps; at launch every warp has 168 (the most
-// that three warps a scheduler allow), and 8 x 200 + 4 x 104 = 12 x 168
-constexpr int kSoftmaxRegs = 200, kIssueRegs = 104;
-constexpr int kPlans = 3;               // items planned ahead
+constexpr int kSoftmaxWarps = 16;
+constexpr int kThreads = 32 * (kSoftmaxWarps + 4);     // two MMA warps, TMA, planner
+constexpr int kPlans = 2;               // items planned ahead
 constexpr unsigned long long kLimitNs = 10000000000ull;
 
 // A work item: kv head; first token and token counts of its tiles; start of
@@ -79,14 +88,15 @@ template <int D> struct Smem {
   static constexpr int kSlots = D == 128 ? 4 : 8;          // two chunks, or four
   static constexpr int kQ = 0;
   static constexpr int kKv = 2 * kBuf;
-  static constexpr int kOut = kKv + kSlots * kBuf;         // 64 dims of each tile's output rows
+  static constexpr int kOut = kKv + kSlots * kBuf;         // [2][2] boxes of 32 dims of a tile's output rows
   static constexpr int kBar = kOut + 2 * kBox;
   // q_full[2] q_empty[2] s_full[2] o_full[2] p_full[2][2] plan_full[]
-  // plan_empty[] kv_full[] kv_empty[]
-  static constexpr int kBars = 12 + 2 * kPlans + 2 * kSlots;
+  // plan_empty[] kv_full[] kv_empty[] pipe[2]
+  static constexpr int kBars = 14 + 2 * kPlans + 2 * kSlots;
   static constexpr int kTmemSlot = kBar + kBars * 8;
   static constexpr int kPlan = kTmemSlot + 16;
-  static constexpr int kBytes = kPlan + kPlans * static_cast<int>(sizeof(Plan)) + 1024;   // + alignment slack
+  static constexpr int kTop = kPlan + kPlans * static_cast<int>(sizeof(Plan));    // bf16 [2][2][128] row maxima
+  static constexpr int kBytes = kTop + 4 * kTile * 2 + 1024;                      // + alignment slack
   static_assert(kBytes <= 232448, "fits one CTA's shared memory");
 };
 
@@ -156,21 +166,24 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait(bar, parity));
 }
 
-// Barriers of the 128 threads of tile x's softmax; tile_all also ANDs a flag.
-__device__ __forceinline__ void tile_sync(int x) {
-  asm volatile("bar.sync %0, 128;" ::"r"(1 + x) : "memory");
-}
-__device__ __forceinline__ bool tile_all(int x, bool flag) {
+// Named barriers of the softmax: the 64 threads that share 32 rows of a tile
+// (1..8), the 256 of a tile (9, 10) and the 128 of a tile's half of the dims
+// (11..14).  The first two also AND a flag, so that a wait that gave up in one
+// warp ends the others that meet it: none is left at a barrier.
+__device__ __forceinline__ bool bar_all(int id, int threads, bool flag) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, %2, 128, p;\n\t"
+      "bar.red.and.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}\n"
       : "=r"(r)
-      : "r"(flag ? 1u : 0u), "r"(1 + x)
+      : "r"(flag ? 1u : 0u), "r"(id), "r"(threads)
       : "memory");
   return r != 0;
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // An item's key chunks.  Chunks 0..nsc-1 cover the sinks [start, start +
@@ -226,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto plan_empty = [&](int e) { return bar0 + 8u * (12 + kPlans + e); };
   auto kv_full = [&](int s) { return bar0 + 8u * (12 + 2 * kPlans + s); };
   auto kv_empty = [&](int s) { return bar0 + 8u * (12 + 2 * kPlans + NS + s); };
+  auto pipe = [&](int x) { return bar0 + 8u * (12 + 2 * kPlans + 2 * NS + x); };
   Plan* plans = reinterpret_cast<Plan*>(sm + SL::kPlan);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + SL::kTmemSlot);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -237,19 +251,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s_full(x), 1);
       mbar_init(p_full(x, 0), 4);        // the tile's four warps
       mbar_init(p_full(x, 1), 4);
+      mbar_init(pipe(x), 1);
       mbar_init(o_full(x), 1);
     }
     for (int e = 0; e < kPlans; ++e) {
       mbar_init(plan_full(e), 1);
-      mbar_init(plan_empty(e), 10);      // the warps that go by plans
+      mbar_init(plan_empty(e), kSoftmaxWarps + 3);      // the warps that go by plans
     }
     for (int s = 0; s < NS; ++s) {
       mbar_init(kv_full(s), 1);
-      mbar_init(kv_empty(s), 1);
+      mbar_init(kv_empty(s), 2);           // both tiles' products
     }
     mbar_init_fence();
   }
-  if (warp == 8) {
+  if (warp == kSoftmaxWarps) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      smem_u32(tmem_slot))
                  : "memory");
@@ -278,11 +293,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
 
-  // (In the issuing roles, flags of the two tiles and the parities of their
-  // barriers are bits x of a word: the loops over x stay rolled.)
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
-    if (warp == 9) {
+  if (warp >= kSoftmaxWarps) {
+    if (warp == kSoftmaxWarps + 2) {
       // ---- TMA producer ----
       const bool lead = elect_one() != 0;
       int slot = 0;                        // of the ring
@@ -349,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < 2 && drained; ++x)
         if ((q_loaded >> x) & 1) drained = wait_warp(q_full(x), ((q_turn >> x) & 1) ^ 1);
     }
-    if (warp == 10) {
+    if (warp == kSoftmaxWarps + 3) {
       // ---- planner ----
       const int end = a.offsets[a.n], pairs = a.items / a.hkv;
       bool again = false, ok = true;       // a plan was in this place before
@@ -395,91 +407,89 @@ __global__ void __launch_bounds__(kThreads, 1)
         publish();
       }
     }
-    if (warp == 8) {
-      // ---- MMA issuer ----
+    if (warp < kSoftmaxWarps + 2) {
+      // ---- MMA issuers, one a tile ----
+      const int x = warp - kSoftmaxWarps;
       const uint32_t lead = elect_one();
       constexpr uint32_t idesc_o = idesc_bf16_f32(kTile, D) | (1u << 16);     // B MN-major
+      const uint32_t d_s = s_at(x), d_o = o_at(x);
+      const uint64_t qd = smem_desc_k_sw128(sbase + SL::kQ + x * SL::kBuf);
       int slot = 0;                        // of the chunk's K; its V lies in the next one
       uint32_t turn = 0;                   // parity of that slot's full barrier
-      uint32_t q_turn = 0, p_turn = 0, s_turn = 0, o_turn = 0;    // bit x
-      // the previous chunk's P V still to be issued, and its V
-      uint32_t todo = 0, opens = 0, closes = 0;
-      int v_slot = 0, v_steps = 0;
+      uint32_t q_turn = 0, p_turn[2] = {0, 0}, s_turn = 0, o_turn = 0;
+      uint32_t pipe_turn = x ^ 1;          // tile 0 begins
+      // the previous chunk's P V, if there is one still to be issued, and its V
+      bool todo = false, opens = false, closes = false, ok = true;
+      int v_slot = -1, v_steps = 0;
       uint32_t v_turn = 0;
-      bool ok = true;
-      auto product = [&](int x) {
-        const uint32_t d = o_at(x), p = s_at(x);
+      auto product = [&]() {
         const uint64_t v = smem_desc_v(sbase + SL::kKv + v_slot * SL::kBuf);
-        const bool fresh = (opens >> x) & 1;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {                     // P comes 64 keys at a time
           if (v_steps <= half * 4) continue;
-          if (!(ok = wait_warp(p_full(x, half), (p_turn >> (2 * x + half)) & 1))) return;
-          p_turn ^= 1u << (2 * x + half);
+          if (!(ok = wait_warp(p_full(x, half), p_turn[half]))) return;
+          p_turn[half] ^= 1;
           tc_fence_after();
           if (v_steps >= half * 4 + 4) {
 #pragma unroll
             for (int k = half * 4; k < half * 4 + 4; ++k)          // 16 keys: 2048 bytes of V
-              mma_ts(lead, d, p + k * 8, v + 128ull * k, idesc_o, !fresh || k > 0);
+              mma_ts(lead, d_o, d_s + half * 64 + (k & 3) * 8, v + 128ull * k, idesc_o, !opens || k > 0);
           } else {
 #pragma unroll 1
-            for (int k = half * 4; k < v_steps; ++k) mma_ts(lead, d, p + k * 8, v + 128ull * k, idesc_o, !fresh || k > 0);
+            for (int k = half * 4; k < v_steps; ++k)
+              mma_ts(lead, d_o, d_s + half * 64 + (k & 3) * 8, v + 128ull * k, idesc_o, !opens || k > 0);
           }
         }
-        if ((closes >> x) & 1) {
+        if (closes) {
           commit(lead, o_full(x));
-          o_turn ^= 1u << x;
+          o_turn ^= 1;
         }
       };
       const Plan* p;
 #pragma unroll 1
       while (ok && next_plan(p)) {
         const Chunks ch(a, *p);
-        const Tile tile0(*p, 0), tile1(*p, 1);
+        const Tile tile(*p, x);
         release_plan();
-        const int last0 = tile0.last(ch), last1 = tile1.last(ch);
-        uint32_t fresh = 3;
+        const int last = tile.last(ch);
+        bool fresh = true;
 #pragma unroll 1
         for (int c = 0; c < ch.nc && ok; ++c) {
           const int kb = ch.base(c), kn = ch.keys(c);
           const int n16 = (kn + 15) / 16;
-          const uint32_t sees = (tile0.sees(a, kb, kn) ? 1u : 0u) | (tile1.sees(a, kb, kn) ? 2u : 0u);
-          const uint32_t ends = (c == last0 ? 1u : 0u) | (c == last1 ? 2u : 0u);
+          const bool sees = tile.sees(a, kb, kn);
           const uint32_t idesc_s = idesc_bf16_f32(kTile, n16 * 16);
           const uint64_t kd = smem_desc_k_sw128(sbase + SL::kKv + slot * SL::kBuf);
-          if (todo != 0 && !(ok = wait_warp(kv_full(v_slot), v_turn))) break;
-          bool k_ready = false;
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!ok) continue;
-            if ((todo >> x) & 1) product(x);
-            if (!ok) continue;
-            if (x == 1 && todo != 0) commit(lead, kv_empty(v_slot));
-            if (!((sees >> x) & 1)) continue;
-            if (((fresh >> x) & 1) && !(ok = wait_warp(q_full(x), (q_turn >> x) & 1))) continue;
-            if (!k_ready && !(ok = wait_warp(kv_full(slot), turn))) continue;
-            k_ready = true;
+          // (A slot is released by both warps once it has been filled, used or
+          // not: a warp that ran ahead would release it for the other.)
+          if (v_slot >= 0 && !(ok = wait_warp(kv_full(v_slot), v_turn))) break;
+          if (!(ok = wait_warp(kv_full(slot), turn))) break;
+          if (!(ok = wait_warp(pipe(x), pipe_turn))) break;
+          pipe_turn ^= 1;
+          if (todo) product();
+          if (!ok) break;
+          if (v_slot >= 0) commit(lead, kv_empty(v_slot));
+          if (sees) {
+            if (fresh && !(ok = wait_warp(q_full(x), q_turn))) break;
             tc_fence_after();
-            const uint64_t qd = smem_desc_k_sw128(sbase + SL::kQ + x * SL::kBuf);
-            const uint32_t d = s_at(x);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {                   // 16 dims: 32 bytes of a box's rows
               const uint64_t off = (ks / 4) * (SL::kBox / 16) + 2ull * (ks % 4);
-              mma_ss(lead, d, qd + off, kd + off, idesc_s, ks > 0);
+              mma_ss(lead, d_s, qd + off, kd + off, idesc_s, ks > 0);
             }
             commit(lead, s_full(x));
-            s_turn ^= 1u << x;
-            if ((ends >> x) & 1) {
+            s_turn ^= 1;
+            if (c == last) {
               commit(lead, q_empty(x));
-              q_turn ^= 1u << x;
+              q_turn ^= 1;
             }
           }
-          if (!ok) break;
+          if (lead) mbar_arrive(pipe(x ^ 1));
           commit(lead, kv_empty(slot));
           todo = sees;
           opens = fresh;
-          closes = ends;
-          fresh &= ~sees;
+          closes = c == last;
+          if (sees) fresh = false;
           v_steps = n16;
           v_turn = turn;
           if ((v_slot = slot + 1) == NS) {
@@ -493,32 +503,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (ok && todo != 0) ok = wait_warp(kv_full(v_slot), v_turn);
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (ok && ((todo >> x) & 1)) product(x);
+      if (ok && todo && wait_warp(kv_full(v_slot), v_turn)) product();
       // tensor memory is freed after the last MMAs have completed (a barrier
       // never used is in phase 0: the wait for parity 1 returns at once)
-      bool drained = true;
-#pragma unroll 1
-      for (int x = 0; x < 2 && drained; ++x)
-        drained = wait_warp(s_full(x), ((s_turn >> x) & 1) ^ 1) && wait_warp(o_full(x), ((o_turn >> x) & 1) ^ 1);
+      if (wait_warp(s_full(x), s_turn ^ 1)) wait_warp(o_full(x), o_turn ^ 1);
     }
   } else {
-    // ---- softmax: one row per thread ----
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const int x = warp >> 2;
-    const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = s_at(x) + quarter, to = o_at(x) + quarter;
-    const int tok = ((warp & 3) * 32 + lane) / a.group;
+    // ---- softmax: half a row per thread ----
+    const int x = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t ts = s_at(x) + lanes + half * 64;         // this half's scores, and P over them
+    const uint32_t to = o_at(x) + lanes + half * (D / 2);    // and its dims of O
+    const int pair_bar = 1 + x * 4 + quarter, tile_bar = 9 + x, dims_bar = 11 + 2 * x + half;
+    bf16* top_at = reinterpret_cast<bf16*>(sm + SL::kTop) + x * 2 * kTile + row;
+    const int tok = row / a.group;
     const uint64_t sc2 = f32x2_splat(a.scale_log2);
     uint32_t s_turn = 0, o_turn = 0;
     bool ok = true;
     const Plan* p;
-    // the tile's four warps take and leave an item together, a wait that gave
-    // up included: none is left at a barrier
 #pragma unroll 1
-    while (tile_all(x, next_plan(p))) {
+    while (bar_all(tile_bar, 256, next_plan(p))) {
       const int h = uni(p->h);
       const Chunks ch(a, *p);
       const Tile tile(*p, x);
@@ -538,168 +543,206 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int all_hi = __reduce_min_sync(0xffffffffu, mine ? t : 0x7fffffff);
       const bool any = __any_sync(0xffffffffu, mine);
       float ref = -INFINITY;             // base-2 reference of the row's exponentials
-      uint64_t l2 = 0ull;
+      uint64_t l2 = 0ull;                // this half's sums
       bool begun = false;
 #pragma unroll 1
       for (int c = 0; c < ch.nc; ++c) {
         const int kb = ch.base(c), kn = ch.keys(c);
         if (!tile.sees(a, kb, kn)) continue;
-        // columns that the row admits, and the 32-key groups that some and
-        // that every row of the warp admits
-        uint32_t in[4];
-        uint32_t some = 0xfu, every = 0xfu;
+        // columns of the half's two 32-key groups that the row admits, and the
+        // groups that some and that every row of the warp admits
+        uint32_t in[2] = {0xffffffffu, 0xffffffffu};
+        bool some[2] = {true, true}, every[2] = {true, true};
         if (!(kn == kTile && kb >= all_lo && kb + kTile - 1 <= all_hi && any)) {
-          some = every = 0;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int b = kb + q * 32;
-            in[q] = !mine ? 0u
-                : low_bits(kn - q * 32) & ((low_bits(t + 1 - b) & ~low_bits(lo - b)) |
-                                           (low_bits(sink_end - b) & ~low_bits(start - b)));
-            if (__any_sync(0xffffffffu, in[q] != 0u)) some |= 1u << q;
-            if (__all_sync(0xffffffffu, in[q] == 0xffffffffu || !mine)) every |= 1u << q;
+          for (int y = 0; y < 2; ++y) {
+            const int q = 64 * half + 32 * y, b = kb + q;
+            in[y] = !mine ? 0u
+                : low_bits(kn - q) & ((low_bits(t + 1 - b) & ~low_bits(lo - b)) |
+                                      (low_bits(sink_end - b) & ~low_bits(start - b)));
+            some[y] = __any_sync(0xffffffffu, in[y] != 0u);
+            every[y] = __all_sync(0xffffffffu, in[y] == 0xffffffffu || !mine);
           }
         }
-        if (!wait_warp(s_full(x), s_turn)) {
-          ok = false;
-          break;
-        }
+        ok = wait_warp(s_full(x), s_turn);
         s_turn ^= 1;
         tc_fence_after();
-        // the row's scores; masked ones become -inf
-        uint32_t s[4][32];
-        tmem_ld_32cols(ts, s[0]);
-        tmem_ld_32cols(ts + 32, s[1]);
-        if (kn > 64) {
-          tmem_ld_32cols(ts + 64, s[2]);
-          tmem_ld_32cols(ts + 96, s[3]);
-        }
-        tmem_wait_ld();
-        float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (!((some >> q) & 1)) continue;
-          if (!((every >> q) & 1)) {
+        // the scores of 32 keys; masked ones become -inf
+        auto load = [&](int y, uint32_t (&s)[32]) {
+          tmem_ld_32cols(ts + y * 32, s);
+          tmem_wait_ld();
+          if (!every[y]) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (!(in[q] & (1u << i))) s[q][i] = 0xff800000u;
+              if (!(in[y] & (1u << i))) s[i] = 0xff800000u;
           }
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            top4[(i / 2) & 3] = fmaxf(fmaxf(top4[(i / 2) & 3], __uint_as_float(s[q][i])), __uint_as_float(s[q][i + 1]));
-        }
-        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * a.scale_log2;
-        const bool move = mine && top > ref + 8.f;
-        if (__any_sync(0xffffffffu, move)) {
-          const float now = move ? top : ref;
-          const float keep = !move ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx_ftz(ref - now));
-          ref = now;
-          l2 = f32x2_mul(l2, f32x2_splat(keep));
-          if (begun) {
-            // the earlier chunks' products are complete: S of this chunk was
-            // issued behind them
+        };
+        uint32_t pk[2][16];
+        uint64_t sum;
+        bool look = !begun;
+        for (;;) {
+          if (look) {
+            // the row's maximum, to bf16 (it only steers the reference; both
+            // threads of the row go by the same two values)
+            float top = -INFINITY;
 #pragma unroll 1
-            for (int q = 0; q < D / 16; ++q) {
-              uint32_t o[16];
-              tmem_ld_16cols(to + q * 16, o);
-              tmem_wait_ld();
+            for (int y = 0; y < 2; ++y) {
+              if (!some[y]) continue;
+              uint32_t s[32];
+              load(y, s);
+              float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-              tmem_st_16cols(to + q * 16, o);
+              for (int i = 0; i < 32; i += 2)
+                m4[(i / 2) & 3] = fmaxf(fmaxf(m4[(i / 2) & 3], __uint_as_float(s[i])), __uint_as_float(s[i + 1]));
+              top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2);
+            }
+            top_at[half * kTile] = __float2bfloat16_rn(top);
+            if (!bar_all(pair_bar, 64, ok)) {
+              ok = false;
+              break;
+            }
+            top = fmaxf(to_f32(top_at[0]), to_f32(top_at[kTile]));
+            const float now = mine ? fmaxf(ref, top) : ref;
+            const float keep = now == ref ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx_ftz(ref - now));
+            ref = now;
+            l2 = f32x2_mul(l2, f32x2_splat(keep));
+            if (begun) {
+              // the earlier chunks' products are complete: S of this chunk was
+              // issued behind them
+#pragma unroll 1
+              for (int q = 0; q < D / 32; ++q) {
+                uint32_t o[16];
+                tmem_ld_16cols(to + q * 16, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                tmem_st_16cols(to + q * 16, o);
+              }
+              tmem_wait_st();
+              tc_fence_before();
             }
           }
-        }
-        begun = true;
-        const uint64_t neg = f32x2_splat(ref == -INFINITY ? 0.f : -ref);
-        uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
+          // P against the reference as it stands, and the maximum beside it
+          const uint64_t neg = f32x2_splat(ref == -INFINITY ? 0.f : -ref);
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (kn <= half * 64) continue;
-#pragma unroll
-          for (int q = 2 * half; q < 2 * half + 2; ++q) {
-            uint32_t pk[16];
-            if ((some >> q) & 1) {
+          for (int y = 0; y < 2; ++y) {
+            if (some[y]) {
+              uint32_t s[32];
+              load(y, s);
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
+                const float s0 = __uint_as_float(s[2 * i]), s1 = __uint_as_float(s[2 * i + 1]);
+                m4[i & 3] = fmaxf(fmaxf(m4[i & 3], s0), s1);
                 float x0, x1;
-                f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(s[q][2 * i]), __uint_as_float(s[q][2 * i + 1])), sc2, neg),
-                             x0, x1);
+                f32x2_unpack(f32x2_fma(f32x2_pack(s0, s1), sc2, neg), x0, x1);
                 const float p0 = ex2_approx_ftz(x0), p1 = ex2_approx_ftz(x1);
                 sum4[i & 3] = f32x2_add(sum4[i & 3], f32x2_pack(p0, p1));
-                pk[i] = pack_bf16x2(p0, p1);
+                pk[y][i] = pack_bf16x2(p0, p1);
               }
             } else {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) pk[i] = 0u;
+              for (int i = 0; i < 16; ++i) pk[y][i] = 0u;
             }
-            tmem_st_16cols(ts + q * 16, pk);
           }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_full(x, half));
+          const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+          sum = f32x2_add(f32x2_add(sum4[0], sum4[1]), f32x2_add(sum4[2], sum4[3]));
+          // Both threads of every row are content with the reference (a bf16
+          // maximum is at most 2^-8 below the maximum itself), and have rescaled
+          // their dims of O.  Else the references move, and the scores, over
+          // which P is not yet laid, are taken again.
+          const float edge = ref == -INFINITY ? ref : ref + 8.f + fabsf(ref) * 0.0078125f;
+          const bool high = mine && top > edge;
+          if (bar_all(pair_bar, 64, ok && !high)) break;
+          look = true;
         }
-        l2 = f32x2_add(l2, f32x2_add(f32x2_add(sum4[0], sum4[1]), f32x2_add(sum4[2], sum4[3])));
+        if (!ok) break;
+        begun = true;
+        if (kn <= 64 * half) continue;
+        l2 = f32x2_add(l2, sum);
+        tmem_st_16cols(ts, pk[0]);
+        tmem_st_16cols(ts + 16, pk[1]);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(x, half));
       }
       if (ok) ok = wait_warp(o_full(x), o_turn);
-      if (!tile_all(x, ok)) break;
       o_turn ^= 1;
       tc_fence_after();
-      float l0, l1;
-      f32x2_unpack(l2, l0, l1);
-      const float inv = 1.f / (l0 + l1);
-      const int head = h * a.group + ((warp & 3) * 32 + lane) % a.group;
-      uint32_t w[D / 2];
+      // the row's sum: the halves' parts meet in a column of S, which is done
+      // with (the last product has read P)
+      float l;
+      {
+        float l0, l1;
+        f32x2_unpack(l2, l0, l1);
+        l = l0 + l1;
+        if (ok) {
+          asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(s_at(x) + lanes + half),
+                       "r"(__float_as_uint(l)) : "memory");
+          tmem_wait_st();
+          tc_fence_before();
+        }
+      }
+      if (!bar_all(tile_bar, 256, ok)) break;
+      tc_fence_after();
+      uint32_t both[2];
+      asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];"
+                   : "=r"(both[0]), "=r"(both[1]) : "r"(s_at(x) + lanes));
+      tmem_wait_ld();
+      const float inv = 1.f / (__uint_as_float(both[0]) + __uint_as_float(both[1]));
+      const int head = h * a.group + row % a.group;
+      uint32_t w[D / 4];
       float worst = 0.f;
 #pragma unroll
       for (int q = 0; q < D / 64; ++q) {
-        uint32_t o[2][32];
-        tmem_ld_32cols(to + q * 64, o[0]);
-        tmem_ld_32cols(to + q * 64 + 32, o[1]);
+        uint32_t o[32];
+        tmem_ld_32cols(to + q * 32, o);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float y0 = __uint_as_float(o[i >> 4][(2 * i) & 31]) * inv, y1 = __uint_as_float(o[i >> 4][(2 * i + 1) & 31]) * inv;
+        for (int i = 0; i < 16; ++i) {
+          const float y0 = __uint_as_float(o[2 * i]) * inv, y1 = __uint_as_float(o[2 * i + 1]) * inv;
           worst = fmaf(y0, 0.f, fmaf(y1, 0.f, worst));      // NaN once one is not finite
-          w[q * 32 + i] = pack_bf16x2(y0, y1);
+          w[q * 16 + i] = pack_bf16x2(y0, y1);
         }
       }
       tc_fence_before();
-      const bool fine = worst == 0.f;
-      const uint32_t odd = __ballot_sync(0xffffffffu, mine && !fine);
-      // A whole tile of finite rows leaves through shared memory, 64 dims at a
+      const uint32_t odd = __ballot_sync(0xffffffffu, mine && worst != 0.f);
+      // A whole tile of finite rows leaves through shared memory, 32 dims at a
       // time, as one box (row by row, a warp's store would touch 32 lines);
-      // other tiles row by row.  (bar.red: the tile's four warps agree.)
-      const bool box = tile_all(x, odd == 0) && tile.t1 - tile.t0 == a.tq;
+      // other tiles row by row.  (Behind this barrier S and O are read.)
+      const bool box = bar_all(tile_bar, 256, odd == 0) && tile.t1 - tile.t0 == a.tq;
       if (box) {
-        const int r = (warp & 3) * 32 + lane;
-        const uint32_t out = sbase + SL::kOut + x * SL::kBox;
+        const uint32_t out = sbase + SL::kOut + (2 * x + half) * (SL::kBox / 2);
 #pragma unroll
         for (int q = 0; q < D / 64; ++q) {
           // the previous box has been read out of shared memory
-          if (r == 0) bulk_wait_group_read<0>();
-          tile_sync(x);
+          if (row == 0) bulk_wait_group_read<0>();
+          bar_sync(dims_bar, 128);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + r * 128 + ((i ^ (r & 7)) << 4)),
-                         "r"(w[q * 32 + 4 * i]), "r"(w[q * 32 + 4 * i + 1]), "r"(w[q * 32 + 4 * i + 2]),
-                         "r"(w[q * 32 + 4 * i + 3])
+          for (int i = 0; i < 4; ++i)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out + row * 64 + ((i ^ ((row >> 1) & 3)) << 4)),
+                         "r"(w[q * 16 + 4 * i]), "r"(w[q * 16 + 4 * i + 1]), "r"(w[q * 16 + 4 * i + 2]),
+                         "r"(w[q * 16 + 4 * i + 3])
                          : "memory");
           fence_proxy_async_smem();
-          tile_sync(x);
-          if (r == 0) {
-            tma_store_3d(&tmo, out, q * 64, h * a.group, tile.t0);
+          bar_sync(dims_bar, 128);
+          if (row == 0) {
+            tma_store_3d(&tmo, out, half * (D / 2) + q * 32, h * a.group, tile.t0);
             bulk_commit_group();
           }
         }
-      } else if (mine) {
-        bf16* dst = a.out + t * a.out_stride + static_cast<int64_t>(head) * D;
+      } else {
+        if (mine) {
+          bf16* dst = a.out + t * a.out_stride + static_cast<int64_t>(head) * D + half * (D / 2);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          for (int i = 0; i < D / 16; ++i)
+            reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+        bar_sync(tile_bar, 256);                // the rows are written before any is written again
       }
       if (odd != 0) {
-        __syncwarp();                           // the rows are written before they are written again
         // does a V row that some row of the tile does not see hold the cause?
         bool cause = false;
         for (int c = 0; c < ch.nc; ++c) {
@@ -740,11 +783,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  if (warp < 8) bulk_wait_group<0>();      // the boxes are written before shared memory goes
+  if (warp < kSoftmaxWarps) bulk_wait_group<0>();      // the boxes are written before shared memory goes
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kSoftmaxWarps) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
@@ -754,10 +797,10 @@ template <int D>
 cudaError_t launch(const WindowArgs& a, int T, int grid, cudaStream_t st) {
   CUtensorMap tq, tk, tv, to;
   const char* why = "";
-  if (!make_tmap_heads(&tq, a.q, T, a.hq, D, a.q_stride, a.group, a.tq, &why) ||
-      !make_tmap_heads(&tk, a.k, T, a.hkv, D, a.k_stride, 1, kTile, &why) ||
-      !make_tmap_heads(&tv, a.v, T, a.hkv, D, a.v_stride, 1, kTile, &why) ||
-      !make_tmap_heads(&to, a.out, T, a.hq, D, a.out_stride, a.group, a.tq, &why))
+  if (!make_tmap_heads(&tq, a.q, T, a.hq, D, a.q_stride, 64, a.group, a.tq, &why) ||
+      !make_tmap_heads(&tk, a.k, T, a.hkv, D, a.k_stride, 64, 1, kTile, &why) ||
+      !make_tmap_heads(&tv, a.v, T, a.hkv, D, a.v_stride, 64, 1, kTile, &why) ||
+      !make_tmap_heads(&to, a.out, T, a.hq, D, a.out_stride, 32, a.group, a.tq, &why))
     return cudaErrorInvalidValue;
   auto kernel = attn_window_kernel<D>;
   const cudaError_t e =

@@ -49,9 +49,11 @@ cudaError_t gemm_launch(const CUtensorMap& a, const CUtensorMap& b, const CUtens
 bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                     uint32_t box_rows, const char** why);
 // 3-D bf16 tensor [rows][heads][dim] whose rows lie row_stride elements apart,
-// box {64 dims, box_heads, box_rows}, 128-byte swizzle, zero fill outside.
+// box {box_dims, box_heads, box_rows} of 64 dims (128-byte swizzle) or 32
+// (64-byte swizzle), zero fill outside.
 bool make_tmap_heads(CUtensorMap* map, const void* base, uint64_t rows, uint64_t heads, uint64_t dim,
-                     uint64_t row_stride, uint32_t box_heads, uint32_t box_rows, const char** why);
+                     uint64_t row_stride, uint32_t box_dims, uint32_t box_heads, uint32_t box_rows,
+                     const char** why);
 // 2-D row-major [rows][cols] output of the GEMM (bf16, or fp32 when f32), box
 // {32 cols, 32 rows}, 64-byte (bf16) or 128-byte (fp32) swizzle: the layout of
 // the GEMM epilogue's staging boxes.  Stores outside the tensor are clipped.

@@ -52,7 +52,8 @@ bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
 }
 
 bool make_tmap_heads(CUtensorMap* map, const void* base, uint64_t rows, uint64_t heads, uint64_t dim,
-                     uint64_t row_stride, uint32_t box_heads, uint32_t box_rows, const char** why) {
+                     uint64_t row_stride, uint32_t box_dims, uint32_t box_heads, uint32_t box_rows,
+                     const char** why) {
   auto fn = encode_fn();
   if (fn == nullptr) {
     *why = "cuTensorMapEncodeTiled is not available from the driver";
@@ -64,11 +65,12 @@ bool make_tmap_heads(CUtensorMap* map, const void* base, uint64_t rows, uint64_t
   }
   const cuuint64_t dims[3] = {dim, heads, rows};
   const cuuint64_t strides[2] = {dim * 2, row_stride * 2};
-  const cuuint32_t box[3] = {64, box_heads, box_rows};
+  const cuuint32_t box[3] = {box_dims, box_heads, box_rows};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        box_dims == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     *why = "cuTensorMapEncodeTiled rejected the tensor";
