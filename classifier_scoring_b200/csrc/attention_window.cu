@@ -36,11 +36,12 @@
 //             and half the code in each).  They read their scores, take the
 //             exponentials with the scale folded into one packed FMA, and write
 //             P as bf16 back to tensor memory.  The reference of the
-//             exponentials is the row's maximum over its first chunk and
-//             follows it only when a later one is 2^8 ahead: then the row's
-//             threads meet over the new maximum, rescale O (in tensor memory,
-//             each half the dims) and take the chunk again, so that otherwise
-//             no exponential waits for a maximum.  32-key groups that every row of a
+//             exponentials is the row's maximum over its first chunk and moves
+//             only after a chunk that was 2^8 ahead of it: then the row's
+//             threads meet over the new maximum and rescale O (in tensor
+//             memory, each half the dims) before the next chunk.  So no
+//             exponential waits for a maximum, nor P for another thread.
+//             32-key groups that every row of a
 //             warp admits take no masks, those that none admits are skipped.
 //             After the last chunk each thread reads half the dims of its row
 //             of O, divides and stores.
@@ -69,6 +70,7 @@ __device__ int32_t g_window_err[ERR_WORDS];
 constexpr int kTile = 128;              // rows of a tile, keys of a chunk
 constexpr int kSoftmaxWarps = 16;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 4);     // two MMA warps, TMA, planner
+constexpr float kLate = 40.f;           // log2; see the softmax
 constexpr int kPlans = 2;               // items planned ahead
 constexpr unsigned long long kLimitNs = 10000000000ull;
 
@@ -468,7 +470,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           pipe_turn ^= 1;
           if (todo) product();
           if (!ok) break;
-          if (v_slot >= 0) commit(lead, kv_empty(v_slot));
           if (sees) {
             if (fresh && !(ok = wait_warp(q_full(x), q_turn))) break;
             tc_fence_after();
@@ -485,6 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (lead) mbar_arrive(pipe(x ^ 1));
+          if (v_slot >= 0) commit(lead, kv_empty(v_slot));
           commit(lead, kv_empty(slot));
           todo = sees;
           opens = fresh;
@@ -544,7 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool any = __any_sync(0xffffffffu, mine);
       float ref = -INFINITY;             // base-2 reference of the row's exponentials
       uint64_t l2 = 0ull;                // this half's sums
-      bool begun = false;
+      bool begun = false, behind = false, set = false, late = false;
+      float last_top = -INFINITY;
 #pragma unroll 1
       for (int c = 0; c < ch.nc; ++c) {
         const int kb = ch.base(c), kn = ch.keys(c);
@@ -577,57 +580,61 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(in[y] & (1u << i))) s[i] = 0xff800000u;
           }
         };
-        uint32_t pk[2][16];
-        uint64_t sum;
-        bool look = !begun;
-        for (;;) {
-          if (look) {
-            // the row's maximum, to bf16 (it only steers the reference; both
-            // threads of the row go by the same two values)
-            float top = -INFINITY;
+        // Rows without a reference that see a key here, and after a chunk whose
+        // maxima left some reference behind: the row's threads meet over its
+        // maximum (to bf16: it only steers the reference, and both go by the
+        // same two values), and what is summed so far is rescaled.
+        const bool sees = mine && ((lo < kb + kn && t >= kb) || (start < kb + kn && sink_end > kb));
+        if (behind || (!set && __any_sync(0xffffffffu, sees && ref == -INFINITY))) {
+          float top = -INFINITY;
 #pragma unroll 1
-            for (int y = 0; y < 2; ++y) {
-              if (!some[y]) continue;
-              uint32_t s[32];
-              load(y, s);
-              float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          for (int y = 0; y < 2; ++y) {
+            if (!(y == 0 ? some[0] : some[1])) continue;
+            uint32_t s[32];
+            load(y, s);
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int i = 0; i < 32; i += 2)
-                m4[(i / 2) & 3] = fmaxf(fmaxf(m4[(i / 2) & 3], __uint_as_float(s[i])), __uint_as_float(s[i + 1]));
-              top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2);
-            }
-            top_at[half * kTile] = __float2bfloat16_rn(top);
-            if (!bar_all(pair_bar, 64, ok)) {
-              ok = false;
-              break;
-            }
-            top = fmaxf(to_f32(top_at[0]), to_f32(top_at[kTile]));
-            const float now = mine ? fmaxf(ref, top) : ref;
-            const float keep = now == ref ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx_ftz(ref - now));
-            ref = now;
-            l2 = f32x2_mul(l2, f32x2_splat(keep));
-            if (begun) {
-              // the earlier chunks' products are complete: S of this chunk was
-              // issued behind them
-#pragma unroll 1
-              for (int q = 0; q < D / 32; ++q) {
-                uint32_t o[16];
-                tmem_ld_16cols(to + q * 16, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                tmem_st_16cols(to + q * 16, o);
-              }
-              tmem_wait_st();
-              tc_fence_before();
-            }
+            for (int i = 0; i < 32; i += 2)
+              m4[(i / 2) & 3] = fmaxf(fmaxf(m4[(i / 2) & 3], __uint_as_float(s[i])), __uint_as_float(s[i + 1]));
+            top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2);
           }
-          // P against the reference as it stands, and the maximum beside it
-          const uint64_t neg = f32x2_splat(ref == -INFINITY ? 0.f : -ref);
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
+          top_at[half * kTile] = __float2bfloat16_rn(fmaxf(top, last_top));
+          if (!bar_all(pair_bar, 64, ok)) {
+            ok = false;
+            break;
+          }
+          top = fmaxf(to_f32(top_at[0]), to_f32(top_at[kTile]));
+          const float now = mine ? fmaxf(ref, top) : ref;
+          const float keep = now == ref ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx_ftz(ref - now));
+          ref = now;
+          l2 = f32x2_mul(l2, f32x2_splat(keep));
+          if (begun) {
+            // the earlier chunks' products are complete: S of this chunk was
+            // issued behind them
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
+              uint32_t o[16];
+              tmem_ld_16cols(to + q * 16, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+              tmem_st_16cols(to + q * 16, o);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+          }
+          set = __all_sync(0xffffffffu, !mine || ref > -INFINITY);
+          bar_sync(pair_bar, 64);        // O is rescaled, and the maxima are read
+        }
+        begun = true;
+        // P against the reference, and the maximum beside it
+        const uint64_t neg = f32x2_splat(ref == -INFINITY ? 0.f : -ref);
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
+        if (kn > 64 * half) {
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
+            uint32_t pk[16];
             if (some[y]) {
               uint32_t s[32];
               load(y, s);
@@ -639,34 +646,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 f32x2_unpack(f32x2_fma(f32x2_pack(s0, s1), sc2, neg), x0, x1);
                 const float p0 = ex2_approx_ftz(x0), p1 = ex2_approx_ftz(x1);
                 sum4[i & 3] = f32x2_add(sum4[i & 3], f32x2_pack(p0, p1));
-                pk[y][i] = pack_bf16x2(p0, p1);
+                pk[i] = pack_bf16x2(p0, p1);
               }
             } else {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) pk[y][i] = 0u;
+              for (int i = 0; i < 16; ++i) pk[i] = 0u;
             }
+            tmem_st_16cols(ts + y * 16, pk);     // over scores that are read
           }
-          const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
-          sum = f32x2_add(f32x2_add(sum4[0], sum4[1]), f32x2_add(sum4[2], sum4[3]));
-          // Both threads of every row are content with the reference (a bf16
-          // maximum is at most 2^-8 below the maximum itself), and have rescaled
-          // their dims of O.  Else the references move, and the scores, over
-          // which P is not yet laid, are taken again.
-          const float edge = ref == -INFINITY ? ref : ref + 8.f + fabsf(ref) * 0.0078125f;
-          const bool high = mine && top > edge;
-          if (bar_all(pair_bar, 64, ok && !high)) break;
-          look = true;
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(x, half));
         }
-        if (!ok) break;
-        begun = true;
-        if (kn <= 64 * half) continue;
-        l2 = f32x2_add(l2, sum);
-        tmem_st_16cols(ts, pk[0]);
-        tmem_st_16cols(ts + 16, pk[1]);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(x, half));
+        l2 = f32x2_add(l2, f32x2_add(f32x2_add(sum4[0], sum4[1]), f32x2_add(sum4[2], sum4[3])));
+        // Has a maximum left its reference behind?  By up to 2^kLate the sums
+        // take it (P and O have the exponents of fp32), and the next chunk moves
+        // the reference; by more, the row is computed again at the end.
+        last_top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+        late = late || (mine && last_top > ref + kLate);
+        const bool high = mine && last_top > ref + 8.f + fabsf(ref) * 0.0078125f;   // (the reference is a bf16)
+        behind = !bar_all(pair_bar, 64, ok && !high);
+        if (behind && !bar_all(pair_bar, 64, ok)) {
+          ok = false;
+          break;
+        }
       }
       if (ok) ok = wait_warp(o_full(x), o_turn);
       o_turn ^= 1;
@@ -708,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
-      const uint32_t odd = __ballot_sync(0xffffffffu, mine && worst != 0.f);
+      const uint32_t odd = __ballot_sync(0xffffffffu, mine && (worst != 0.f || late));
       // A whole tile of finite rows leaves through shared memory, 32 dims at a
       // time, as one box (row by row, a warp's store would touch 32 lines);
       // other tiles row by row.  (Behind this barrier S and O are read.)
@@ -759,8 +763,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (__any_sync(0xffffffffu, cause)) {
-          for (uint32_t left = odd; left != 0; left &= left - 1) {
+        const uint32_t again = __any_sync(0xffffffffu, cause) ? odd : odd & __ballot_sync(0xffffffffu, late);
+        {
+          for (uint32_t left = again; left != 0; left &= left - 1) {
             const int src = __ffs(left) - 1;
             const int64_t tt = __shfl_sync(0xffffffffu, t, src);
             const int64_t hh = __shfl_sync(0xffffffffu, head, src);
