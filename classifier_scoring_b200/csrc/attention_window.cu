@@ -154,6 +154,12 @@ __device__ __forceinline__ uint64_t smem_desc_v(uint32_t saddr) {
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (1024ull << 16) | (64ull << 32) |
          (1ull << 46) | (2ull << 61);
 }
+// the larger of three, in one instruction
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t low_bits(int x) {
   return x <= 0 ? 0u : (x >= 32 ? 0xffffffffu : ((1u << x) - 1u));
 }
@@ -545,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int all_hi = __reduce_min_sync(0xffffffffu, mine ? t : 0x7fffffff);
       const bool any = __any_sync(0xffffffffu, mine);
       float ref = -INFINITY;             // base-2 reference of the row's exponentials
-      uint64_t l2 = 0ull;                // this half's sums
+      float l = 0.f;                     // this half's sum
       bool begun = false, behind = false, set = false, late = false;
       float last_top = -INFINITY;
 #pragma unroll 1
@@ -567,6 +573,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             every[y] = __all_sync(0xffffffffu, in[y] == 0xffffffffu || !mine);
           }
         }
+        // Rows without a reference that see a key here, and after a chunk whose
+        // maxima left some reference behind: the row's threads meet over its
+        // maximum (to bf16: it only steers the reference, and both go by the
+        // same two values), and what is summed so far is rescaled.
+        const bool sees = mine && ((lo < kb + kn && t >= kb) || (start < kb + kn && sink_end > kb));
+        const bool look = behind || (!set && __any_sync(0xffffffffu, sees && ref == -INFINITY));
         ok = wait_warp(s_full(x), s_turn);
         s_turn ^= 1;
         tc_fence_after();
@@ -580,12 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(in[y] & (1u << i))) s[i] = 0xff800000u;
           }
         };
-        // Rows without a reference that see a key here, and after a chunk whose
-        // maxima left some reference behind: the row's threads meet over its
-        // maximum (to bf16: it only steers the reference, and both go by the
-        // same two values), and what is summed so far is rescaled.
-        const bool sees = mine && ((lo < kb + kn && t >= kb) || (start < kb + kn && sink_end > kb));
-        if (behind || (!set && __any_sync(0xffffffffu, sees && ref == -INFINITY))) {
+        if (look) {
           float top = -INFINITY;
 #pragma unroll 1
           for (int y = 0; y < 2; ++y) {
@@ -595,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < 32; i += 2)
-              m4[(i / 2) & 3] = fmaxf(fmaxf(m4[(i / 2) & 3], __uint_as_float(s[i])), __uint_as_float(s[i + 1]));
+              m4[(i / 2) & 3] = max3(m4[(i / 2) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
             top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2);
           }
           top_at[half * kTile] = __float2bfloat16_rn(fmaxf(top, last_top));
@@ -607,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float now = mine ? fmaxf(ref, top) : ref;
           const float keep = now == ref ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx_ftz(ref - now));
           ref = now;
-          l2 = f32x2_mul(l2, f32x2_splat(keep));
+          l *= keep;
           if (begun) {
             // the earlier chunks' products are complete: S of this chunk was
             // issued behind them
@@ -630,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // P against the reference, and the maximum beside it
         const uint64_t neg = f32x2_splat(ref == -INFINITY ? 0.f : -ref);
         float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        uint64_t sum4[4] = {0ull, 0ull, 0ull, 0ull};
+        float sum4[4] = {0.f, 0.f, 0.f, 0.f};
         if (kn > 64 * half) {
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
@@ -641,11 +648,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const float s0 = __uint_as_float(s[2 * i]), s1 = __uint_as_float(s[2 * i + 1]);
-                m4[i & 3] = fmaxf(fmaxf(m4[i & 3], s0), s1);
+                m4[i & 3] = max3(m4[i & 3], s0, s1);
                 float x0, x1;
                 f32x2_unpack(f32x2_fma(f32x2_pack(s0, s1), sc2, neg), x0, x1);
                 const float p0 = ex2_approx_ftz(x0), p1 = ex2_approx_ftz(x1);
-                sum4[i & 3] = f32x2_add(sum4[i & 3], f32x2_pack(p0, p1));
+                sum4[(i & 1) * 2] += p0;
+                sum4[(i & 1) * 2 + 1] += p1;
                 pk[i] = pack_bf16x2(p0, p1);
               }
             } else {
@@ -659,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(p_full(x, half));
         }
-        l2 = f32x2_add(l2, f32x2_add(f32x2_add(sum4[0], sum4[1]), f32x2_add(sum4[2], sum4[3])));
+        l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
         // Has a maximum left its reference behind?  By up to 2^kLate the sums
         // take it (P and O have the exponents of fp32), and the next chunk moves
         // the reference; by more, the row is computed again at the end.
@@ -677,17 +685,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       // the row's sum: the halves' parts meet in a column of S, which is done
       // with (the last product has read P)
-      float l;
-      {
-        float l0, l1;
-        f32x2_unpack(l2, l0, l1);
-        l = l0 + l1;
-        if (ok) {
-          asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(s_at(x) + lanes + half),
-                       "r"(__float_as_uint(l)) : "memory");
-          tmem_wait_st();
-          tc_fence_before();
-        }
+      if (ok) {
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(s_at(x) + lanes + half),
+                     "r"(__float_as_uint(l)) : "memory");
+        tmem_wait_st();
+        tc_fence_before();
       }
       if (!bar_all(tile_bar, 256, ok)) break;
       tc_fence_after();
