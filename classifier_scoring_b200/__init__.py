@@ -208,16 +208,20 @@ def _on_one_device(*xs) -> list:
     """The addresses of device buffers; tensors among them must lie on one CUDA device."""
     found, dev = [], None
     for x in xs:
-        if x is None or type(x) is int:
-            found.append(x)
+        if x is None:
+            found.append(None)
             continue
-        if hasattr(x, "get_device"):
+        try:
             d = x.get_device()
-            if dev is None:
-                dev = d
-            if d != dev or d < 0:
+            p = x.data_ptr()
+        except AttributeError:                 # an address
+            found.append(_ptr(x))
+            continue
+        if d != dev:
+            if dev is not None or d < 0:
                 raise RmError(RM_E_INVAL, "every buffer must be memory of the same CUDA device")
-        found.append(_ptr(x))
+            dev = d
+        found.append(p)
     return found
 
 

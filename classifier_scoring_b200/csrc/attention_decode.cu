@@ -636,7 +636,8 @@ cudaError_t launch(DecodeArgs a, int num_sms, cudaStream_t st) {
   const int64_t most = static_cast<int64_t>(a.n) * a.units * ((keys + SH::kTile - 1) / SH::kTile + kUnitCost);
   const int grid = static_cast<int>(std::min<int64_t>(most, std::min(kMaxCtas, num_sms * kCtasPerSm)));
   auto kernel = attn_decode_kernel<D, E, NH>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::kSmem);
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_smem(kernel, SH::kSmem, allowed);
   if (e != cudaSuccess) return e;
   kernel<<<grid, kThreads, SH::kSmem, st>>>(a);
   e = cudaGetLastError();

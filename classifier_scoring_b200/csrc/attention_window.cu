@@ -810,8 +810,8 @@ cudaError_t launch(const WindowArgs& a, int T, int grid, cudaStream_t st) {
       !make_tmap_heads(&to, a.out, T, a.hq, D, a.out_stride, 32, a.group, a.tq, &why))
     return cudaErrorInvalidValue;
   auto kernel = attn_window_kernel<D>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+  static std::atomic<unsigned long long> allowed{0};
+  const cudaError_t e = allow_smem(kernel, Smem<D>::kBytes, allowed);
   if (e != cudaSuccess) return e;
   kernel<<<grid, kThreads, Smem<D>::kBytes, st>>>(tq, tk, tv, to, a);
   return cudaGetLastError();

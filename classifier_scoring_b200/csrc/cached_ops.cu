@@ -1,5 +1,6 @@
 // C ABI of the incremental-scoring steps (include/rm_ops.h): validation and
 // launch.
+#include <atomic>
 #include <cmath>
 
 #include "common.cuh"
@@ -9,6 +10,17 @@
 namespace rmk {
 namespace {
 
+// The SM count of a device, looked up once (0: not yet).
+cudaError_t device_sms(int dev, int* out) {
+  static std::atomic<int> known[kMaxDevices];
+  const bool keep = dev >= 0 && dev < kMaxDevices;
+  *out = keep ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (*out != 0) return cudaSuccess;
+  const cudaError_t e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && keep) known[dev].store(*out, std::memory_order_relaxed);
+  return e;
+}
+
 // An output pointer is memory of the current device: a call made with another
 // device current, or with host buffers, is refused rather than left to fault.
 // (One pointer a call: the driver takes 0.4 us to look one up.)
@@ -17,8 +29,7 @@ int check_on_device(const void* out, int* num_sms = nullptr) {
   cudaError_t e = cudaGetDevice(&dev);
   cudaPointerAttributes at;
   if (e == cudaSuccess) e = cudaPointerGetAttributes(&at, out);
-  if (e == cudaSuccess && num_sms != nullptr)
-    e = cudaDeviceGetAttribute(num_sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && num_sms != nullptr) e = device_sms(dev, num_sms);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return set_error(RM_E_DEVICE, "no usable CUDA device: %s", cudaGetErrorString(e));

@@ -21,6 +21,7 @@ namespace {
 // whose barrier separates the reads from the writes.
 // ---------------------------------------------------------------------------
 constexpr int kSlotRun = 8;
+constexpr int kMaxSlotSeqs = 16384;
 
 // x / P = x * mul >> shift for 0 <= x < 2^31, P = 1..1024 (2^shift = 2^31 * the
 // power of two from P on: the multiplier fits 32 bits and exceeds 2^shift / P
@@ -248,6 +249,24 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(const Rop
   const int c = lane % LP, sub = lane / LP;   // this lane's dims 8c..8c+7 of its head
   const bool live = 8 * c < a.d;
   const int h0 = part * a.per_part, h1 = min(a.heads, h0 + a.per_part);
+  // the row's heads by kind, this warp's share of each: [from[k], from[k+1]) of
+  // queries, keys, values
+  const int qk = a.hq + a.hkv;
+  const int from[4] = {h0, min(max(h0, a.hq), h1), min(max(h0, qk), h1), h1};
+  const bf16* src = a.qkv + t * a.qkv_stride + 8 * c + static_cast<int64_t>(sub) * a.d;
+  const int step = kPer * a.d;
+  // A batch of heads is loaded while the one before it is worked on, the first
+  // one under the trigonometry.
+  uint4 raw[kRopeBatch];
+  auto load = [&](int h, int hb) {
+#pragma unroll
+    for (int b = 0; b < kRopeBatch; ++b)
+      if (live && h + sub + b * kPer < hb) raw[b] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(h) * a.d + b * step);
+  };
+  {
+    const int k = from[1] > from[0] ? 0 : (from[2] > from[1] ? 1 : 2);
+    load(from[k], from[k + 1]);
+  }
   const int half = a.rot / 2;
   uint64_t cs[4], sn[4];                      // of the lane's dims: y = x cs + partner sn
   if (half > 0) {
@@ -297,9 +316,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(const Rop
 
   // heads [ha, hb) of one kind; head h of the row is head h - first of its
   // kind, written to out (row of this token, or null) and to the cache
-  auto section = [&](auto kind, int ha, int hb, int first, const float* gain_at, bf16* out, E* cache,
+  auto section = [&](auto kind, const int k, int first, const float* gain_at, bf16* out, E* cache,
                      const float* scale) {
     constexpr bool kValue = decltype(kind)::value;
+    const int ha = from[k], hb = from[k + 1];
     if (ha >= hb) return;
     const bool norm = !kValue && gain_at != nullptr;
     uint64_t gain[4];
@@ -311,24 +331,22 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(const Rop
       gain[2] = f32x2_pack(g1.x, g1.y);
       gain[3] = f32x2_pack(g1.z, g1.w);
     }
-    const bf16* src = a.qkv + t * a.qkv_stride + 8 * c + static_cast<int64_t>(ha + sub) * a.d;
-    const int step = kPer * a.d, cache_head = a.page_size * a.d;
+    const int cache_head = a.page_size * a.d;
     int own = ha + sub - first;               // this lane's head among its kind
     bf16* dst = out == nullptr ? nullptr : out + static_cast<int64_t>(own) * a.d + 8 * c;
     E* cdst = cache == nullptr ? nullptr : cache + cache_row + static_cast<int64_t>(own) * cache_head + 8 * c;
     for (int h = ha + sub; h - sub < hb; h += kRopeBatch * kPer) {
-      uint4 raw[kRopeBatch];
+      uint4 now[kRopeBatch];
 #pragma unroll
-      for (int b = 0; b < kRopeBatch; ++b) {
-        raw[b] = make_uint4(0u, 0u, 0u, 0u);
-        if (live && h + b * kPer < hb) raw[b] = *reinterpret_cast<const uint4*>(src + b * step);
-      }
-      src += kRopeBatch * step;
+      for (int b = 0; b < kRopeBatch; ++b) now[b] = live && h + b * kPer < hb ? raw[b] : make_uint4(0u, 0u, 0u, 0u);
+      if (h - sub + kRopeBatch * kPer < hb) load(h - sub + kRopeBatch * kPer, hb);
+      else if (k < 2 && from[k + 2] > hb) load(hb, from[k + 2]);
+      else if (k < 1) load(from[2], from[3]);
 #pragma unroll
       for (int b = 0; b < kRopeBatch; ++b) {
         if (h - sub + b * kPer >= hb) break;
-        uint64_t x[4] = {f32x2_pack(bf16_lo(raw[b].x), bf16_hi(raw[b].x)), f32x2_pack(bf16_lo(raw[b].y), bf16_hi(raw[b].y)),
-                         f32x2_pack(bf16_lo(raw[b].z), bf16_hi(raw[b].z)), f32x2_pack(bf16_lo(raw[b].w), bf16_hi(raw[b].w))};
+        uint64_t x[4] = {f32x2_pack(bf16_lo(now[b].x), bf16_hi(now[b].x)), f32x2_pack(bf16_lo(now[b].y), bf16_hi(now[b].y)),
+                         f32x2_pack(bf16_lo(now[b].z), bf16_hi(now[b].z)), f32x2_pack(bf16_lo(now[b].w), bf16_hi(now[b].w))};
         if (norm) {
           uint64_t ss2 = f32x2_mul(x[0], x[0]);
 #pragma unroll
@@ -399,14 +417,11 @@ __global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(const Rop
   };
   using Turned = std::integral_constant<bool, false>;
   using Value = std::integral_constant<bool, true>;
-  const int qk = a.hq + a.hkv;
   E* kc = cache_row < 0 ? nullptr : static_cast<E*>(a.kc);
-  section(Turned{}, h0, min(h1, a.hq), 0, a.q_gain, a.q_out + t * a.q_stride, static_cast<E*>(nullptr), nullptr);
-  if (kc != nullptr || a.k_out != nullptr)
-    section(Turned{}, max(h0, a.hq), min(h1, qk), a.hq, a.k_gain, a.k_out == nullptr ? nullptr : a.k_out + t * a.k_stride, kc,
-            a.k_scale);
-  if (kc != nullptr)
-    section(Value{}, max(h0, qk), h1, qk, nullptr, static_cast<bf16*>(nullptr), static_cast<E*>(a.vc), a.v_scale);
+  E* vc = cache_row < 0 ? nullptr : static_cast<E*>(a.vc);
+  section(Turned{}, 0, 0, a.q_gain, a.q_out + t * a.q_stride, static_cast<E*>(nullptr), nullptr);
+  section(Turned{}, 1, a.hq, a.k_gain, a.k_out == nullptr ? nullptr : a.k_out + t * a.k_stride, kc, a.k_scale);
+  section(Value{}, 2, qk, nullptr, static_cast<bf16*>(nullptr), vc, a.v_scale);
 }
 
 template <typename E, int LP> cudaError_t rope_go(RopeArgs a, int num_sms, cudaStream_t st) {
@@ -433,8 +448,8 @@ cudaError_t kv_slots_launch(const int32_t* len_before, const int32_t* n_new, int
                             int32_t* used_after, int32_t* unserved, cudaStream_t st) {
   const size_t smem = (3 * static_cast<size_t>(n) + 2) * 4;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        kv_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static std::atomic<unsigned long long> allowed{0};
+    const cudaError_t e = allow_smem(kv_slots_kernel, (3 * kMaxSlotSeqs + 2) * 4, allowed);
     if (e != cudaSuccess) return e;
   }
   PageDiv div;
