@@ -13,8 +13,9 @@
 // key once, and short sequences still fill a tile.  Tiles do not care for
 // sequence borders: a row admits the keys of its own sequence and window, and
 // the item's keys are one range of packed rows, plus the first sequence's
-// sinks when its window has left them behind.  Items are dealt to one
-// persistent CTA per SM, the last tokens (which see most) first:
+// sinks when its window has left them behind.  One block runs per SM and,
+// as it gets to them, takes over the items of the blocks that are not launched
+// yet (cluster launch control), the last tokens (which see most) first:
 //   warp 19 : plans items ahead of the others: key range, chunks and the start of
 //             each row's sequence (searches in the offsets) into shared memory;
 //   warp 18 : TMA -- the two Q tiles of an item and, per 128-key chunk, K and V
@@ -93,9 +94,10 @@ template <int D> struct Smem {
   static constexpr int kOut = kKv + kSlots * kBuf;         // [2][2] boxes of 32 dims of a tile's output rows
   static constexpr int kBar = kOut + 2 * kBox;
   // q_full[2] q_empty[2] s_full[2] o_full[2] p_full[2][2] plan_full[]
-  // plan_empty[] kv_full[] kv_empty[] pipe[2]
-  static constexpr int kBars = 14 + 2 * kPlans + 2 * kSlots;
-  static constexpr int kTmemSlot = kBar + kBars * 8;
+  // plan_empty[] kv_full[] kv_empty[] pipe[2] claimed
+  static constexpr int kBars = 15 + 2 * kPlans + 2 * kSlots;
+  static constexpr int kClaim = (kBar + kBars * 8 + 15) / 16 * 16;
+  static constexpr int kTmemSlot = kClaim + 16;
   static constexpr int kPlan = kTmemSlot + 16;
   static constexpr int kTop = kPlan + kPlans * static_cast<int>(sizeof(Plan));    // bf16 [2][2][128] row maxima
   static constexpr int kBytes = kTop + 4 * kTile * 2 + 1024;                      // + alignment slack
@@ -262,6 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(pipe(x), 1);
       mbar_init(o_full(x), 1);
     }
+    mbar_init(pipe(2), 1);               // the planner's claims
     for (int e = 0; e < kPlans; ++e) {
       mbar_init(plan_full(e), 1);
       mbar_init(plan_empty(e), kSoftmaxWarps + 3);      // the warps that go by plans
@@ -371,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == kSoftmaxWarps + 3) {
       // ---- planner ----
-      const int end = a.offsets[a.n], pairs = a.items / a.hkv;
+      const int end = min(a.offsets[a.n], a.tmax), pairs = a.items / a.hkv;
       bool again = false, ok = true;       // a plan was in this place before
       uint32_t turn = 1;
       auto begin = [&]() { return !again || wait_warp(plan_empty(plan), turn); };
@@ -384,31 +387,61 @@ __global__ void __launch_bounds__(kThreads, 1)
           again = true;
         }
       };
+      const uint32_t claim = sbase + SL::kClaim, claimed = pipe(2);
+      uint32_t claim_turn = 0;
+      int item = blockIdx.x;
 #pragma unroll 1
-      for (int item = blockIdx.x; item < a.items && ok; item += gridDim.x) {
+      while (ok) {
         const int t0 = (pairs - 1 - item / a.hkv) * 2 * a.tq;
         const int count = min(2 * a.tq, end - t0);
-        if (count <= 0) continue;
-        if (!(ok = begin())) break;
-        Plan& p = plans[plan];
+        if (count > 0) {
+          if (!(ok = begin())) break;
+          Plan& p = plans[plan];
 #pragma unroll 2
-        for (int i = lane; i < count; i += 32) {
-          const int t = t0 + i;
-          const int start = a.offsets[upper_index(a.offsets, a.n, t)];
-          p.begins[i] = static_cast<uint8_t>(max(0, start - t0));
-          if (i == 0 || i == a.tq) {
-            const int x = i == 0 ? 0 : 1;
-            p.start[x] = start;
-            p.lo[x] = a.window > 0 ? max(start, t - a.window + 1) : start;
+          for (int i = lane; i < count; i += 32) {
+            const int t = t0 + i;
+            const int start = max(0, min(t, a.offsets[upper_index(a.offsets, a.n, t)]));
+            p.begins[i] = static_cast<uint8_t>(max(0, start - t0));
+            if (i == 0 || i == a.tq) {
+              const int x = i == 0 ? 0 : 1;
+              p.start[x] = start;
+              p.lo[x] = a.window > 0 ? max(start, t - a.window + 1) : start;
+            }
           }
+          if (lane == 0) {
+            p.h = item % a.hkv;
+            p.t0 = t0;
+            p.count[0] = min(count, a.tq);
+            p.count[1] = count - p.count[0];
+          }
+          publish();
         }
+        // the next item: the block of this grid that would have been launched
+        // next is taken over instead (none left: this one is the last)
         if (lane == 0) {
-          p.h = item % a.hkv;
-          p.t0 = t0;
-          p.count[0] = min(count, a.tq);
-          p.count[1] = count - p.count[0];
+          mbar_arrive_expect_tx(claimed, 16);
+          asm volatile(
+              "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(claim),
+              "r"(claimed)
+              : "memory");
         }
-        publish();
+        if (!(ok = wait_warp(claimed, claim_turn))) break;
+        claim_turn ^= 1;
+        uint32_t taken, block;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+            "ld.shared.b128 r, [%2];\n\t"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t"
+            "mov.u32 %1, 0;\n\t"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}\n"
+            : "=r"(taken), "=r"(block)
+            : "r"(claim)
+            : "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (!__any_sync(0xffffffffu, taken != 0)) break;
+        item = static_cast<int>(block);
       }
       if (ok && begin()) {
         if (lane == 0) plans[plan].h = -1;
@@ -846,8 +879,9 @@ cudaError_t attn_window_launch(const void* q, int64_t q_stride, const void* k, i
   const int64_t items = (static_cast<int64_t>(T) + 2 * a.tq - 1) / (2 * a.tq) * hkv;
   if (items > 0x7fffffff) return cudaErrorInvalidValue;
   a.items = static_cast<int>(items);
-  const int grid = std::min(a.items, num_sms);
-  return d == 64 ? launch<64>(a, T, grid, st) : launch<128>(a, T, grid, st);
+  (void)num_sms;
+  // a block an item: those that run take the others over (planner)
+  return d == 64 ? launch<64>(a, T, a.items, st) : launch<128>(a, T, a.items, st);
 }
 
 }  // namespace rmk
