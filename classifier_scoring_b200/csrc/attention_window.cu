@@ -99,7 +99,7 @@ template <int D> struct Smem {
   static constexpr int kClaim = (kBar + kBars * 8 + 15) / 16 * 16;
   static constexpr int kTmemSlot = kClaim + 16;
   static constexpr int kPlan = kTmemSlot + 16;
-  static constexpr int kTop = kPlan + kPlans * static_cast<int>(sizeof(Plan));    // bf16 [2][2][128] row maxima
+  static constexpr int kTop = kPlan + kPlans * static_cast<int>(sizeof(Plan));    // 128 bytes for each two softmax warps
   static constexpr int kBytes = kTop + 4 * kTile * 2 + 1024;                      // + alignment slack
   static_assert(kBytes <= 232448, "fits one CTA's shared memory");
 };
@@ -557,7 +557,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = s_at(x) + lanes + half * 64;         // this half's scores, and P over them
     const uint32_t to = o_at(x) + lanes + half * (D / 2);    // and its dims of O
     const int pair_bar = 1 + x * 4 + quarter, tile_bar = 9 + x, dims_bar = 11 + 2 * x + half;
-    bf16* top_at = reinterpret_cast<bf16*>(sm + SL::kTop) + x * 2 * kTile + row;
+    // 128 bytes where the pair's threads meet, over a maximum (bf16, both
+    // halves') or a sum: written before a barrier, read behind it, with another
+    // barrier before they are written again
+    bf16* top_at = reinterpret_cast<bf16*>(sm + SL::kTop + (x * 4 + quarter) * 128) + lane;
+    float* sum_at = reinterpret_cast<float*>(sm + SL::kTop + (x * 4 + quarter) * 128) + lane;
     const int tok = row / a.group;
     const uint64_t sc2 = f32x2_splat(a.scale_log2);
     uint32_t s_turn = 0, o_turn = 0;
@@ -638,12 +642,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               m4[(i / 2) & 3] = max3(m4[(i / 2) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
             top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2);
           }
-          top_at[half * kTile] = __float2bfloat16_rn(fmaxf(top, last_top));
+          top_at[half * 32] = __float2bfloat16_rn(fmaxf(top, last_top));
           if (!bar_all(pair_bar, 64, ok)) {
             ok = false;
             break;
           }
-          top = fmaxf(to_f32(top_at[0]), to_f32(top_at[kTile]));
+          top = fmaxf(to_f32(top_at[0]), to_f32(top_at[32]));
           const float now = mine ? fmaxf(ref, top) : ref;
           const float keep = now == ref ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx_ftz(ref - now));
           ref = now;
@@ -716,21 +720,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) ok = wait_warp(o_full(x), o_turn);
       o_turn ^= 1;
       tc_fence_after();
-      // the row's sum: the halves' parts meet in a column of S, which is done
-      // with (the last product has read P)
-      if (ok) {
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(s_at(x) + lanes + half),
-                     "r"(__float_as_uint(l)) : "memory");
-        tmem_wait_st();
-        tc_fence_before();
-      }
+      // the row's sum: the second half's part to the first, and back (not in a
+      // column of S: the next item's scores may be on their way there)
+      if (half == 1) *sum_at = l;
+      bar_sync(pair_bar, 64);
+      if (half == 0) *sum_at = l + *sum_at;
       if (!bar_all(tile_bar, 256, ok)) break;
-      tc_fence_after();
-      uint32_t both[2];
-      asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];"
-                   : "=r"(both[0]), "=r"(both[1]) : "r"(s_at(x) + lanes));
-      tmem_wait_ld();
-      const float inv = 1.f / (__uint_as_float(both[0]) + __uint_as_float(both[1]));
+      const float inv = 1.f / *sum_at;
       const int head = h * a.group + row % a.group;
       uint32_t w[D / 4];
       float worst = 0.f;
