@@ -99,8 +99,8 @@ template <int D> struct Smem {
   static constexpr int kClaim = (kBar + kBars * 8 + 15) / 16 * 16;
   static constexpr int kTmemSlot = kClaim + 16;
   static constexpr int kPlan = kTmemSlot + 16;
-  static constexpr int kTop = kPlan + kPlans * static_cast<int>(sizeof(Plan));    // 128 bytes for each two softmax warps
-  static constexpr int kBytes = kTop + 4 * kTile * 2 + 1024;                      // + alignment slack
+  static constexpr int kMeet = kPlan + kPlans * static_cast<int>(sizeof(Plan));   // 128 bytes for each two softmax warps
+  static constexpr int kBytes = kMeet + kSoftmaxWarps / 2 * 128 + 1024;           // + alignment slack
   static_assert(kBytes <= 232448, "fits one CTA's shared memory");
 };
 
@@ -557,11 +557,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = s_at(x) + lanes + half * 64;         // this half's scores, and P over them
     const uint32_t to = o_at(x) + lanes + half * (D / 2);    // and its dims of O
     const int pair_bar = 1 + x * 4 + quarter, tile_bar = 9 + x, dims_bar = 11 + 2 * x + half;
-    // 128 bytes where the pair's threads meet, over a maximum (bf16, both
-    // halves') or a sum: written before a barrier, read behind it, with another
-    // barrier before they are written again
-    bf16* top_at = reinterpret_cast<bf16*>(sm + SL::kTop + (x * 4 + quarter) * 128) + lane;
-    float* sum_at = reinterpret_cast<float*>(sm + SL::kTop + (x * 4 + quarter) * 128) + lane;
+    // where a row's two threads meet, over a maximum or a sum: the second half's
+    // part goes to the first, and the whole back, each between two barriers
+    float* meet = reinterpret_cast<float*>(sm + SL::kMeet + (x * 4 + quarter) * 128) + lane;
     const int tok = row / a.group;
     const uint64_t sc2 = f32x2_splat(a.scale_log2);
     uint32_t s_turn = 0, o_turn = 0;
@@ -612,8 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // Rows without a reference that see a key here, and after a chunk whose
         // maxima left some reference behind: the row's threads meet over its
-        // maximum (to bf16: it only steers the reference, and both go by the
-        // same two values), and what is summed so far is rescaled.
+        // maximum, and what is summed so far is rescaled.
         const bool sees = mine && ((lo < kb + kn && t >= kb) || (start < kb + kn && sink_end > kb));
         const bool look = behind || (!set && __any_sync(0xffffffffu, sees && ref == -INFINITY));
         ok = wait_warp(s_full(x), s_turn);
@@ -642,12 +639,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               m4[(i / 2) & 3] = max3(m4[(i / 2) & 3], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
             top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2);
           }
-          top_at[half * 32] = __float2bfloat16_rn(fmaxf(top, last_top));
+          top = fmaxf(top, last_top);
+          if (half == 1) *meet = top;
           if (!bar_all(pair_bar, 64, ok)) {
             ok = false;
             break;
           }
-          top = fmaxf(to_f32(top_at[0]), to_f32(top_at[32]));
+          if (half == 0) *meet = fmaxf(top, *meet);
+          bar_sync(pair_bar, 64);
+          top = *meet;
           const float now = mine ? fmaxf(ref, top) : ref;
           const float keep = now == ref ? 1.f : (ref == -INFINITY ? 0.f : ex2_approx_ftz(ref - now));
           ref = now;
@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the reference; by more, the row is computed again at the end.
         last_top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
         late = late || (mine && last_top > ref + kLate);
-        const bool high = mine && last_top > ref + 8.f + fabsf(ref) * 0.0078125f;   // (the reference is a bf16)
+        const bool high = mine && last_top > ref + 8.f;
         behind = !bar_all(pair_bar, 64, ok && !high);
         if (behind && !bar_all(pair_bar, 64, ok)) {
           ok = false;
@@ -722,11 +722,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       // the row's sum: the second half's part to the first, and back (not in a
       // column of S: the next item's scores may be on their way there)
-      if (half == 1) *sum_at = l;
+      if (half == 1) *meet = l;
       bar_sync(pair_bar, 64);
-      if (half == 0) *sum_at = l + *sum_at;
+      if (half == 0) *meet = l + *meet;
       if (!bar_all(tile_bar, 256, ok)) break;
-      const float inv = 1.f / *sum_at;
+      const float inv = 1.f / *meet;
       const int head = h * a.group + row % a.group;
       uint32_t w[D / 4];
       float worst = 0.f;
