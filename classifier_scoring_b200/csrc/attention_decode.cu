@@ -376,10 +376,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
         top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], w));
         top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], w));
       }
-      // The reference the exponentials are taken against follows the maximum
-      // only when it falls 2^8 behind: a rescale of the output is then rare, and
-      // P stays below 2^8 with the same relative rounding.
-      if (__any_sync(0xffffffffu, top[0] > m[nh][0] + 8.f || top[1] > m[nh][1] + 8.f)) {
+      // The reference is the running maximum itself: the largest probability is
+      // then 1, which has no rounding.  It seldom moves, and only then is the
+      // output rescaled.
+      if (__any_sync(0xffffffffu, top[0] > m[nh][0] || top[1] > m[nh][1])) {
         float keep[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
