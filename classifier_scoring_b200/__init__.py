@@ -9,6 +9,7 @@ is not built this module raises on first use; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import weakref
 from typing import Optional
@@ -204,8 +205,17 @@ def _ptr(x) -> Optional[int]:
     return int(x)
 
 
+_DATA_PTR, _GET_DEVICE = operator.methodcaller("data_ptr"), operator.methodcaller("get_device")
+
+
 def _on_one_device(*xs) -> list:
     """The addresses of device buffers; tensors among them must lie on one CUDA device."""
+    try:                                       # all tensors: the common case of a step's call
+        found = set(map(_GET_DEVICE, xs))
+        if len(found) == 1 and found.pop() >= 0:
+            return list(map(_DATA_PTR, xs))
+    except AttributeError:
+        pass
     found, dev = [], None
     for x in xs:
         if x is None:
@@ -506,9 +516,7 @@ class ops:
     def qk_norm_rope(qkv, qkv_stride, q_out, q_stride, k_out, k_stride, T, n_q_heads, n_kv_heads, head_dim,
                      q_gain, k_gain, eps, rope, positions, cache=None, slots=None, stream=None):
         """rope: Rope or None; cache: KvCache or None; k_out may be None."""
-        x, qo, ko, gq, gk, pos, sl, _, _ = _on_one_device(
-            qkv, q_out, k_out, q_gain, k_gain, positions, slots, None if rope is None else rope._keep,
-            None if cache is None else cache._keep[0])
+        x, qo, ko, gq, gk, pos, sl = _on_one_device(qkv, q_out, k_out, q_gain, k_gain, positions, slots)
         _check(lib().rm_op_qk_norm_rope(x, qkv_stride, qo, q_stride, ko, k_stride, T, n_q_heads, n_kv_heads,
                                         head_dim, gq, gk, eps, None if rope is None else rope._ref, pos,
                                         None if cache is None else cache._ref, sl, _stream(stream)))
@@ -534,7 +542,7 @@ class ops:
         """workspace: device buffer of attn_decode_workspace(...) bytes (its size is read from a tensor)."""
         if workspace_bytes is None:
             workspace_bytes = workspace.numel() * workspace.element_size()
-        q, tab, ln, o, ws, _ = _on_one_device(q, block_table, length, out, workspace, cache._keep[0])
+        q, tab, ln, o, ws = _on_one_device(q, block_table, length, out, workspace)
         _check(lib().rm_op_attn_decode(q, q_stride, cache._ref, tab, table_stride, ln, n_seqs, n_q_heads, window,
                                        sinks, o, out_stride, ws, workspace_bytes, _stream(stream)))
 

@@ -23,7 +23,7 @@ cudaError_t device_sms(int dev, int* out) {
 
 // An output pointer is memory of the current device: a call made with another
 // device current, or with host buffers, is refused rather than left to fault.
-// (One pointer a call: the driver takes 0.4 us to look one up.)
+// (One pointer a call: looking all of slot maps' eleven up took 2 us of 8.)
 int check_on_device(const void* out, int* num_sms = nullptr) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
