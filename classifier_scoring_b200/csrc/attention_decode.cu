@@ -280,11 +280,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   const int g = lane >> 2, t2 = (lane & 3) * 2;
   uint32_t qf[NH][D / 16][2];
   float sc[NH][2], m[NH][2], l[NH][2], o[D / 16][NH][4];
-  auto begin_unit = [&]() {
+  // A unit's queries are asked for before the unit ahead of it is joined and
+  // written, and made ready (8-bit caches) and its state reset behind that.
+  auto load_queries = [&]() {
     const int h = use.u / mtiles, r0 = (use.u % mtiles) * kRows;
     const int rows = min(kRows, group - r0);
     const bf16* q = a.q + use.s * a.q_stride + static_cast<int64_t>(h * group + r0) * D;
-    const float ks = a.scale_log2 * (kF8 && a.k_scale != nullptr ? a.k_scale[h] : 1.f);
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
       const int r = nh * 8 + g;
@@ -297,6 +298,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
           const int dim = k * 16 + (kF8 ? 2 * t2 + x * 2 : t2 + x * 8);
           qf[nh][k][x] = r < rows ? *reinterpret_cast<const uint32_t*>(q + r * D + dim) : 0u;
         }
+    }
+  };
+  auto begin_unit = [&]() {
+    const float ks = a.scale_log2 * (kF8 && a.k_scale != nullptr ? a.k_scale[use.u / mtiles] : 1.f);
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
       sc[nh][0] = sc[nh][1] = ks;
       if (kF8) {
         // bf16 queries as fp16, times the power of two that brings the head's
@@ -443,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   // Joins the warps' states of a finished unit, in warp order, and writes the
   // output rows, or the unit's part when the stretch holds only part of it.
   // As many warps as the buffer has room for write at once.
-  auto end_unit = [&](long long unit0, bool whole) {
-    const int h = use.u / mtiles, r0 = (use.u % mtiles) * kRows;
+  auto end_unit = [&](int s, int u, long long unit0, bool whole) {
+    const int h = u / mtiles, r0 = (u % mtiles) * kRows;
     const int rows = min(kRows, group - r0);
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh)
@@ -507,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       }
       if (whole) {
         const float inv = lt == 0.f ? 0.f : vs / lt;
-        *reinterpret_cast<uint32_t*>(a.out + use.s * a.out_stride + static_cast<int64_t>(h * group + r0 + r) * D + d2) =
+        *reinterpret_cast<uint32_t*>(a.out + s * a.out_stride + static_cast<int64_t>(h * group + r0 + r) * D + d2) =
             pack_bf16x2(x0 * inv, x1 * inv);
       } else {
         *reinterpret_cast<float2*>(po + r * D + d2) = make_float2(x0, x1);
@@ -529,6 +536,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
+  load_queries();
   begin_unit();
   int stage = 0;
   int4 rec = make_int4(-1, 0, 0, 0);
@@ -544,18 +552,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     stage = stage + 1 == kStages ? 0 : stage + 1;
     const bool last_of_unit = use.t + 1 == use.seen.nt;
     const bool last = last_of_unit ? use.v + 1 + kUnitCost >= v1 : use.v + 1 >= v1;
-    if (last_of_unit || last) {
-      const long long unit0 = use.v - use.t - kUnitCost;      // the unit's first place
-      const bool begins = unit0 + kUnitCost >= first;         // its first tile is in this stretch
-      end_unit(unit0, begins && last_of_unit);
-      if (!last_of_unit && begins) {                          // it goes on in the next stretches
-        const long long end = unit0 + kUnitCost + use.seen.nt;
-        rec = make_int4(use.s, use.u, unit0 + kUnitCost <= first ? 0 : 1, static_cast<int>((end * ctas - 1) / total));
-      }
+    if (!last_of_unit && !last) {
+      use.next(a, SH::kTile);
+      continue;
     }
+    const int s = use.s, u = use.u;
+    const long long unit0 = use.v - use.t - kUnitCost;        // the unit's first place
+    const bool begins = unit0 + kUnitCost >= first;           // its first tile is in this stretch
+    if (!last_of_unit && begins) {                            // it goes on in the next stretches
+      const long long end = unit0 + kUnitCost + use.seen.nt;
+      rec = make_int4(s, u, unit0 + kUnitCost <= first ? 0 : 1, static_cast<int>((end * ctas - 1) / total));
+    }
+    if (!last) {
+      use.next(a, SH::kTile);
+      load_queries();
+    }
+    end_unit(s, u, unit0, begins && last_of_unit);
     if (last) break;
-    use.next(a, SH::kTile);
-    if (last_of_unit) begin_unit();
+    begin_unit();
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (tid == 0) a.parts.rec[c] = rec;

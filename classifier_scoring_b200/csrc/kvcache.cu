@@ -201,7 +201,12 @@ __global__ void __launch_bounds__(1024, 1)
 // ---------------------------------------------------------------------------
 constexpr int kRopeWarps = 4;
 constexpr int kRopeMaxDim = 256;
-constexpr int kRopeBatch = 4;                 // loads a lane has in flight
+// Loads a lane has in flight, and blocks per SM that the registers allow: long
+// heads take more loads, short ones (whose warps are soon done) more warps.
+template <int LP> struct RopeShape {
+  static constexpr int kBatch = LP >= 16 ? 4 : 2;
+  static constexpr int kBlocks = LP >= 16 ? 4 : 5;
+};
 
 struct RopeArgs {
   const bf16* qkv;
@@ -238,7 +243,8 @@ __device__ __forceinline__ void store_cache8(__nv_fp8_e4m3* p, const float* f, f
 }
 
 template <typename E, int LP>
-__global__ void __launch_bounds__(kRopeWarps * 32) qk_norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<LP>::kBlocks) qk_norm_rope_kernel(const RopeArgs a) {
+  constexpr int kRopeBatch = RopeShape<LP>::kBatch;
   __shared__ __align__(16) float trig[kRopeWarps][2][kRopeMaxDim / 2];
   __shared__ __align__(16) float swap[kRopeWarps][32 * 8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -89,9 +89,10 @@ def test_slots(n, lo, hi, far, page, in_place):
                C.kv_slots(before, new, page, free, 2, table, T))
 
 
-def test_slots_of_the_most_sequences():
+@pytest.mark.parametrize("in_place", [False, True])
+def test_slots_of_the_most_sequences(in_place):
     before, new, free, table, T = slots_case(16384, 0, 3, 30, 8, 5)
-    same_slots(run_slots(before, new, free, table, T, 8), C.kv_slots(before, new, 8, free, 2, table, T))
+    same_slots(run_slots(before, new, free, table, T, 8, in_place=in_place), C.kv_slots(before, new, 8, free, 2, table, T))
 
 
 @pytest.mark.parametrize("what", ["pages", "tokens", "row", "negative length", "negative count", "used", "used beyond", "no pages"])
@@ -304,10 +305,92 @@ def test_attn_window_head_layouts(hq, hkv, d):
     window_case([70, 1, 31, 150], hq, hkv, d, 50, 3, seed=hq)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_attn_window_of_nothing_writes_nothing(d):
+    window_case([0, 0], 4, 2, d, 40, 2, extra=300)
+
+
 @pytest.mark.parametrize("d,pad,extra", [(64, 8, 0), (128, 64, 5), (64, 0, 200), (128, 8, 1)])
 def test_attn_window_strides_and_rows_behind(d, pad, extra):
     window_case([5, 131, 90], 4, 2, d, 40, 2, pad=pad, extra=extra)
     window_case([300], 2, 2, d, 0, 0, pad=pad, extra=extra)
+
+
+def window_on_device(q, k, v, off, window, sinks):
+    """attend_window of the oracle in fp64 on the device, a sequence and a head at a time (for batches of many work items)."""
+    T, hq, d = q.shape
+    out, mag = torch.zeros(T, hq, d, dtype=torch.float64, device="cuda"), torch.zeros(T, hq, d, dtype=torch.float64, device="cuda")
+    top = torch.zeros(T, hq, dtype=torch.float64, device="cuda")
+    for a, b in zip(off[:-1], off[1:]):
+        if a == b:
+            continue
+        i, j = torch.arange(b - a, device="cuda")[:, None], torch.arange(b - a, device="cuda")[None]
+        seen = (j <= i) & ((j > i - window) | (j < sinks)) if window > 0 else j <= i
+        for h in range(hq):
+            kk, vv, qq = (x[a:b, y].double() for x, y in ((k, h // (hq // k.shape[1])), (v, h // (hq // k.shape[1])), (q, h)))
+            p = torch.softmax((qq @ kk.T / d ** 0.5).masked_fill(~seen, -float("inf")), -1)
+            out[a:b, h], mag[a:b, h] = p @ vv, p @ vv.abs()
+            top[a:b, h] = ((qq.abs() @ kk.abs().T) / d ** 0.5).masked_fill(~seen, 0).amax(-1)
+    return out.cpu().numpy(), mag.cpu().numpy(), top.cpu().numpy()
+
+
+@pytest.mark.parametrize("n,lo,hi,hq,hkv,d,window,sinks", [
+    (60, 1, 200, 12, 12, 64, 0, 0), (40, 100, 300, 16, 16, 128, 60, 4), (3, 900, 2500, 8, 1, 128, 300, 2),
+    (200, 0, 40, 10, 10, 128, 16, 1), (9, 100, 900, 15, 3, 64, 200, 70), (400, 1, 3, 6, 2, 128, 0, 0)])
+def test_attn_window_of_many_items(n, lo, hi, hq, hkv, d, window, sinks):
+    # more work items than SMs: blocks take one after the other, tiles keep their barriers' turns across items
+    lens = np.random.RandomState(n).randint(lo, hi + 1, n)
+    off = np.concatenate([[0], np.cumsum(lens)])
+    T = int(off[-1])
+    q, k, v = (randn((T, h, d), n + i) for i, h in enumerate((hq, hkv, hkv)))
+    ref, mag, top = window_on_device(q, k, v, off, window, sinks)
+    dev_off = dev(off, torch.int32)
+    outs = []
+    for _ in range(3):
+        out = torch.full((T, hq * d), NAN, dtype=torch.bfloat16, device="cuda")
+        rm.ops.attn_window(q, hq * d, k, hkv * d, v, hkv * d, dev_off, n, T, hq, hkv, d, window, sinks, out, hq * d)
+        outs.append(out)
+    torch.cuda.synchronize()
+    err, bound = np.abs(f64(outs[0]).reshape(T, hq, d) - ref), attention_bound(ref, mag, top)
+    assert np.all(err <= bound), (float(np.nanmax(err / bound)), np.argwhere(~(err <= bound))[:3])
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+def test_attn_window_captured_replayed_and_on_two_streams():
+    # a captured call on buffers that change, and two calls at once on streams of their own
+    lens, hq, hkv, d = [200, 1, 77, 300], 8, 4, 128
+    off = np.concatenate([[0], np.cumsum(lens)])
+    T = int(off[-1])
+    dev_off = dev(off, torch.int32)
+    sets = [tuple(randn((T, h * d), 7 * s + i) for i, h in enumerate((hq, hkv, hkv))) for s in range(2)]
+
+    def call(x, out, stream=None):
+        rm.ops.attn_window(x[0], hq * d, x[1], hkv * d, x[2], hkv * d, dev_off, len(lens), T, hq, hkv, d, 50, 3, out, hq * d, stream=stream)
+
+    want = []
+    for x in sets:
+        out = torch.empty(T, hq * d, dtype=torch.bfloat16, device="cuda")
+        call(x, out)
+        want.append(out)
+    torch.cuda.synchronize()
+    x = tuple(t.clone() for t in sets[0])
+    out = torch.full_like(want[0], NAN)
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=s):
+        call(x, out, s)
+    for which in (1, 0, 1):
+        for a, b in zip(x, sets[which]):
+            a.copy_(b)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[which])
+    streams, outs = [torch.cuda.Stream(), torch.cuda.Stream()], [torch.full_like(out, NAN), torch.full_like(out, NAN)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for y, o, st in zip(sets, outs, streams):
+            call(y, o, st)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
 
 
 @pytest.mark.parametrize("scale", [4.0, 20.0, 1e-3])
@@ -461,6 +544,14 @@ def test_attn_decode_head_layouts(hq, hkv, d, kind):
 @pytest.mark.parametrize("page", [16, 48])
 def test_attn_decode_window_and_sinks(window, sinks, kind, d, page):
     decode_case([1, 5, 16, 99, 100, 101, 640, 1500, 0], 4, 2, d, page, window, sinks, kind, seed=window)
+
+
+@pytest.mark.parametrize("hq,hkv,d,kind", [(4, 4, 128, "bf16"), (24, 2, 64, "e4m3"), (8, 1, 128, "e4m3")])
+def test_attn_decode_of_many_short_sequences_beside_a_long_one(hq, hkv, d, kind):
+    # stretches of many units, and units over many stretches
+    lens = [int(x) for x in np.random.RandomState(hq).randint(0, 70, 400)]
+    lens[123] = 20000
+    decode_case(lens, hq, hkv, d, 16, kind=kind, seed=1)
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
