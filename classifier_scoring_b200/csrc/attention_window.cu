@@ -223,8 +223,10 @@ struct Tile {
       : t0(uni(p.t0 + (x == 0 ? 0 : p.count[0]))), t1(uni(p.t0 + p.count[0] + (x == 0 ? 0 : p.count[1]))),
         start(uni(p.start[x])), lo(uni(p.lo[x])) {}
   __device__ __forceinline__ bool sees(const WindowArgs& a, int b, int keys) const {
-    return t1 > t0 && b < t1 && (b + keys > lo || (b - start < a.sinks && b + keys > start));
+    return t1 > t0 && keys > 0 && (b + keys > lo || (b - start < a.sinks && b + keys > start));
   }
+  // of a chunk's keys from b on, those up to the tile's last token
+  __device__ __forceinline__ int keys(const Chunks& c, int i, int b) const { return min(c.keys(i), t1 - b); }
   __device__ __forceinline__ int last(const Chunks& c) const { return c.nsc + (t1 - 1 - c.lo) / kTile; }
 };
 
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool fresh = true;
 #pragma unroll 1
         for (int c = 0; c < ch.nc && ok; ++c) {
-          const int kb = ch.base(c), kn = ch.keys(c);
+          const int kb = ch.base(c), kn = tile.keys(ch, c, kb);
           const int n16 = (kn + 15) / 16;
           const bool sees = tile.sees(a, kb, kn);
           const uint32_t idesc_s = idesc_bf16_f32(kTile, n16 * 16);
@@ -591,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float last_top = -INFINITY;
 #pragma unroll 1
       for (int c = 0; c < ch.nc; ++c) {
-        const int kb = ch.base(c), kn = ch.keys(c);
+        const int kb = ch.base(c), kn = tile.keys(ch, c, kb);
         if (!tile.sees(a, kb, kn)) continue;
         // columns of the half's two 32-key groups that the row admits, and the
         // groups that some and that every row of the warp admits
@@ -781,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // does a V row that some row of the tile does not see hold the cause?
         bool cause = false;
         for (int c = 0; c < ch.nc; ++c) {
-          const int kb = ch.base(c), kn = ch.keys(c);
+          const int kb = ch.base(c), kn = tile.keys(ch, c, kb);
           if (!tile.sees(a, kb, kn) || (kb >= all_lo && kb + kn - 1 <= all_hi)) continue;
           const int rows = min(((kn + 15) / 16) * 16, a.tmax - kb);      // what the products read
           for (int j = lane; j < rows; j += 32) {
