@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   __shared__ uint32_t masks[kWarps][kStages];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
+  pdl_wait();
 
   // this CTA's stretch [v0, v1) of all places, and where it begins
   const int per = (a.n + kThreads - 1) / kThreads;
@@ -653,11 +654,10 @@ cudaError_t launch(DecodeArgs a, int num_sms, cudaStream_t st) {
   static std::atomic<unsigned long long> allowed{0};
   cudaError_t e = allow_smem(kernel, SH::kSmem, allowed);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, SH::kSmem, st>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // the join starts while the first kernel drains and waits for it
   PdlScope pdl(true);
+  e = launch_k(kernel, dim3(grid), dim3(kThreads), SH::kSmem, st, a);
+  if (e != cudaSuccess) return e;
+  // the join is launched while the first kernel drains, and waits for it
   return launch_k(attn_decode_join_kernel<D, NH>, dim3(grid, std::min(SH::kRows, group)), dim3(kJoinThreads), 0, st, a,
                   static_cast<int>(sizeof(E) == 1));
 }

@@ -286,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait();
   const uint32_t tmem = *tmem_slot;
   auto s_at = [&](int x) { return tmem + static_cast<uint32_t>(x * kTile); };
   auto o_at = [&](int x) { return tmem + static_cast<uint32_t>(2 * kTile + x * kTile); };
@@ -844,8 +845,8 @@ cudaError_t launch(const WindowArgs& a, int T, int grid, cudaStream_t st) {
   static std::atomic<unsigned long long> allowed{0};
   const cudaError_t e = allow_smem(kernel, Smem<D>::kBytes, allowed);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, Smem<D>::kBytes, st>>>(tq, tk, tv, to, a);
-  return cudaGetLastError();
+  PdlScope pdl(true);
+  return launch_k(kernel, dim3(grid), dim3(kThreads), Smem<D>::kBytes, st, tq, tk, tv, to, a);
 }
 
 }  // namespace

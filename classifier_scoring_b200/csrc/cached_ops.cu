@@ -1,5 +1,8 @@
 // C ABI of the incremental-scoring steps (include/rm_ops.h): validation and
-// launch.
+// launch.  Their kernels are launched with programmatic stream serialization
+// (launched while the kernel ahead of them drains) and wait for that kernel
+// before they touch global memory; only the decode kernel lets its dependent,
+// the join, be launched early.
 #include <atomic>
 #include <cmath>
 

@@ -54,6 +54,7 @@ __global__ void __launch_bounds__(1024, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int threads = blockDim.x, P = div.P;
   if (tid == 0) first_bad = n;
+  pdl_wait();
   const int used = *used_before;
 
   // each thread sums a stretch of requests, then the stretches are scanned.
@@ -248,6 +249,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<LP>::kBlocks) qk_no
   __shared__ __align__(16) float trig[kRopeWarps][2][kRopeMaxDim / 2];
   __shared__ __align__(16) float swap[kRopeWarps][32 * 8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp;
   const int t = static_cast<int>(item / a.parts), part = static_cast<int>(item % a.parts);
   if (t >= a.T) return;
@@ -441,8 +443,8 @@ template <typename E, int LP> cudaError_t rope_go(RopeArgs a, int num_sms, cudaS
   a.parts = (steps + per - 1) / per;
   const int64_t ctas = (static_cast<int64_t>(a.T) * a.parts + kRopeWarps - 1) / kRopeWarps;
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-  qk_norm_rope_kernel<E, LP><<<static_cast<unsigned>(ctas), kRopeWarps * 32, 0, st>>>(a);
-  return cudaGetLastError();
+  PdlScope pdl(true);
+  return launch_k(qk_norm_rope_kernel<E, LP>, dim3(static_cast<unsigned>(ctas)), dim3(kRopeWarps * 32), 0, st, a);
 }
 
 }  // namespace
@@ -471,17 +473,19 @@ cudaError_t kv_slots_launch(const int32_t* len_before, const int32_t* n_new, int
   const int threads = n > 4096 ? 1024 : 256;
   int ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(148, (runs + threads - 1) / threads)));
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   const bool cluster = in_place && ctas > 1;
-  if (cluster) attr[0].val.clusterDim.x = ctas = 8;
+  if (cluster) attr[1].val.clusterDim.x = ctas = 8;
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(cluster ? 1024 : threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = cluster ? 1 : 0;
+  cfg.numAttrs = cluster ? 2 : 1;
   const bool wide = ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slots)) & 15) == 0;
   return cudaLaunchKernelEx(&cfg, kv_slots_kernel, len_before, n_new, n, div, free_pages, n_free,
                             used_before, block_table, stride, T, offsets, positions, slots,
