@@ -196,8 +196,9 @@ __global__ void __launch_bounds__(1024, 1)
 // heads when there are few tokens: the token's cosines and sines are computed
 // once per warp and stay in registers for all its heads, as do the gains.
 // LP lanes (a power of two from head_dim / 8 on) hold a head, eight dims each;
-// a rotation's partner dims are exchanged through shared memory, which takes
-// any rot_dim.  No two warps meet, and a head is read whole before it is
+// a rotation's partner dims come by a shuffle where they lie a power of two of
+// lanes away (26k tokens of 48 heads of 128: 144 us through shared memory), else
+// through shared memory, which takes any rot_dim.  No two warps meet, and a head is read whole before it is
 // written, so the outputs may lie over the input.
 // ---------------------------------------------------------------------------
 constexpr int kRopeWarps = 4;
@@ -221,6 +222,7 @@ struct RopeArgs {
   float eps, inv_d;
   const double* freqs;
   int rot, interleaved;
+  int swap_lanes;                             // rot / 16 where that is a power of two, else 0
   float mscale;
   const int32_t* positions;
   void *kc, *vc;
@@ -375,6 +377,9 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<LP>::kBlocks) qk_no
               f32x2_unpack(x[e], lo, hi);
               y[e] = f32x2_pack(hi, lo);
             }
+          } else if (a.swap_lanes != 0) {     // the partner chunk is a fixed lane away
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = __shfl_xor_sync(0xffffffffu, x[e], a.swap_lanes);
           } else {
             __syncwarp();
             reinterpret_cast<ulonglong2*>(mine)[0] = make_ulonglong2(x[0], x[1]);
@@ -518,6 +523,8 @@ cudaError_t qk_norm_rope_launch(const void* qkv, int64_t qkv_stride, void* q_out
   a.freqs = rope.freqs;
   a.rot = rope.rot_dim;
   a.interleaved = rope.layout;
+  const int apart = rope.rot_dim % 16 == 0 ? rope.rot_dim / 16 : 0;
+  a.swap_lanes = (apart & (apart - 1)) == 0 ? apart : 0;
   a.mscale = rope.mscale;
   a.positions = positions;
   a.kc = cache.k;
