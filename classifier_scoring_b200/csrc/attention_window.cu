@@ -785,8 +785,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool cause = false;
         for (int c = 0; c < ch.nc; ++c) {
           const int kb = ch.base(c), kn = tile.keys(ch, c, kb);
-          if (!tile.sees(a, kb, kn) || (kb >= all_lo && kb + kn - 1 <= all_hi)) continue;
           const int rows = min(((kn + 15) / 16) * 16, a.tmax - kb);      // what the products read
+          if (!tile.sees(a, kb, kn) || (kb >= all_lo && kb + rows - 1 <= all_hi)) continue;
           for (int j = lane; j < rows; j += 32) {
             const bf16* vr = a.v + (kb + j) * a.v_stride + h * D;
             for (int e = 0; e < D / 8; ++e) {

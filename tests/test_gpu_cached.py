@@ -316,6 +316,14 @@ def test_attn_window_strides_and_rows_behind(d, pad, extra):
     window_case([300], 2, 2, d, 0, 0, pad=pad, extra=extra)
 
 
+@pytest.mark.parametrize("lens,hq", [([17], 8), ([100], 32), ([37], 64), ([65], 4), ([3, 97, 1], 16), ([200], 128)])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (130, 1)])
+def test_attn_window_nan_rows_behind_a_tile_of_one_token(lens, hq, d, window, sinks):
+    # the last tile's warps all hold the last token: every key they are given is seen, what the MMA reads behind it is not
+    window_case(lens, hq, 1, d, window, sinks, extra=40)
+
+
 def window_on_device(q, k, v, off, window, sinks):
     """attend_window of the oracle in fp64 on the device, a sequence and a head at a time (for batches of many work items)."""
     T, hq, d = q.shape
