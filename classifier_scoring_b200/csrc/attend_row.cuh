@@ -3,6 +3,8 @@
 // others.
 #pragma once
 
+#include <cfloat>
+
 #include "common.cuh"
 
 namespace rmk {
@@ -37,7 +39,8 @@ __device__ __forceinline__ void attend_keys(const bf16* q, float scale, int64_t 
     }
     const uint32_t seen = __ballot_sync(0xffffffffu, kp != nullptr);
     if (seen == 0) continue;
-    const float mn = fmaxf(r.m, group_max<32>(s));
+    // (scores of -inf alone: any finite reference makes their weights 0)
+    const float mn = fmaxf(fmaxf(r.m, group_max<32>(s)), -FLT_MAX);
     const float keep = r.l == 0.f ? 0.f : exp2f(r.m - mn);
     const float p = kp != nullptr ? exp2f(s - mn) : 0.f;
     r.m = mn;

@@ -324,6 +324,25 @@ def test_attn_window_nan_rows_behind_a_tile_of_one_token(lens, hq, d, window, si
     window_case(lens, hq, 1, d, window, sinks, extra=40)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("spoil", [False, True])
+def test_attn_window_scores_of_minus_infinity(d, spoil):
+    # keys whose score is -inf weigh nothing beside finite ones; rows that see no others are NaN (0 / 0)
+    T, first = 300, 150
+    q, k, v = torch.ones(T, d, dtype=torch.bfloat16, device="cuda"), randn((T, d), 4), randn((T, d), 5)
+    k[:first, 3] = -float("inf")
+    if spoil:
+        v[T - 1] = NAN                            # rows before the last are computed again from what they see
+    out = torch.empty(T, d, dtype=torch.bfloat16, device="cuda")
+    rm.ops.attn_window(q, d, k, d, v, d, dev([0, T], torch.int32), 1, T, 1, 1, d, 0, 0, out, d)
+    torch.cuda.synchronize()
+    got, last = f64(out).reshape(T, 1, d), T - spoil
+    x = [f64(t).reshape(T, 1, d)[first:last] for t in (q, k, v)]
+    ref, mag, top = C.attend_window(*x, [0, last - first], 0, 0)
+    assert np.isnan(got[:first]).all() and np.isnan(got[last:]).all()
+    assert np.all(np.abs(got[first:last] - ref) <= attention_bound(ref, mag, top))
+
+
 def window_on_device(q, k, v, off, window, sinks):
     """attend_window of the oracle in fp64 on the device, a sequence and a head at a time (for batches of many work items)."""
     T, hq, d = q.shape
