@@ -20,6 +20,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
   const int lr = lane & 7, lm = lane >> 3;
   auto step = [&](int stage) {
     const uint32_t kb = ring_u + stage * 2 * SH::kHalf, vb = kb + SH::kHalf;
-    const uint32_t mask = masks[warp][stage] >> g;              // of keys g, g + 8, ...
+    const uint32_t keys = masks[warp][stage], mask = keys >> g;  // of keys g, g + 8, ...
     float s[kKeys / 16][NH][4];
 #pragma unroll
     for (int kt = 0; kt < kKeys / 16; ++kt) {
@@ -367,10 +368,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
         }
       }
     }
-    // base-2 scores: elements 0, 1 of key 16 kt + g, 2, 3 of key 16 kt + 8 + g
+    // base-2 scores: elements 0, 1 of key 16 kt + g, 2, 3 of key 16 kt + 8 + g.
+    // Once a key is seen the reference is finite: scores of -inf weigh nothing,
+    // and a row of them alone ends as 0 / 0, unlike one that saw no key.
+    const float floor = keys != 0u ? -FLT_MAX : -INFINITY;
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
-      float top[2] = {-INFINITY, -INFINITY};
+      float top[2] = {floor, floor};
 #pragma unroll
       for (int kt = 0; kt < kKeys / 16; ++kt)
 #pragma unroll
@@ -514,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
         x1 += v.y;
       }
       if (whole) {
-        const float inv = lt == 0.f ? 0.f : vs / lt;
+        const float inv = lt == 0.f && mt == -INFINITY ? 0.f : vs / lt;       // no key: zeros
         *reinterpret_cast<uint32_t*>(a.out + s * a.out_stride + static_cast<int64_t>(h * group + r0 + r) * D + d2) =
             pack_bf16x2(x0 * inv, x1 * inv);
       } else {
@@ -627,7 +631,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const De
     for (int i = 1; i < kGroups; ++i) acc += red[i][dim];
     const float vs = f8 && a.v_scale != nullptr ? a.v_scale[h] : 1.f;
     a.out[rec.x * a.out_stride + static_cast<int64_t>(h * group + r0 + r) * D + dim] =
-        __float2bfloat16_rn(lt == 0.f ? 0.f : acc * (vs / lt));
+        __float2bfloat16_rn(lt == 0.f && mt == -INFINITY ? 0.f : acc * (vs / lt));
   }
 }
 

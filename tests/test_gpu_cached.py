@@ -655,6 +655,25 @@ def test_attn_decode_infinite_scores_in_a_seen_key_are_nan_as_defined():
     assert torch.isfinite(out[0]).all() and torch.isnan(out[1, 3]) and torch.isfinite(out[1, :3]).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("L,first", [(1, 1), (40, 40), (300, 299), (300, 150), (5000, 5000), (5000, 4990)])
+def test_attn_decode_scores_of_minus_infinity(d, L, first):
+    # as in the windowed attention: -inf weighs nothing beside a finite score, and nothing else to see is NaN
+    k, v = randn((L, 1, d), 4), randn((L, 1, d), 5)
+    k[:first, 0, 3] = -float("inf")
+    cache, _, _, table = paged([k], [v], 16, 4)
+    q = torch.ones(1, d, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros(1, d, dtype=torch.bfloat16, device="cuda")
+    space = torch.empty(rm.ops.attn_decode_workspace(1, 1, cache), dtype=torch.uint8, device="cuda")
+    rm.ops.attn_decode(q, d, cache, dev(table, torch.int32), table.shape[1], dev([L], torch.int32), 1, 1, 0, 0, out, d, space)
+    torch.cuda.synchronize()
+    if first == L:
+        assert torch.isnan(out).all()
+    else:
+        ref, mag, top = C.attend(f64(q), f64(k)[first:], f64(v)[first:], np.arange(L - first))
+        assert np.all(np.abs(f64(out) - ref) <= attention_bound(ref, mag, top))
+
+
 def test_offsets_beyond_32_bits():
     # a cache of over 2^32 elements: pages at its two ends, written through slots and read back
     hkv, d, page = 8, 128, 16
