@@ -109,7 +109,7 @@ class Rope:
     gives the host values).  Keeps the buffer alive."""
 
     def __init__(self, freqs, rot_dim, *, layout=ROPE_HALF, mscale=1.0):
-        self._args = _RopeArgs(_ptr(freqs), rot_dim, layout, mscale)
+        self._args = _RopeArgs(*_on_one_device(freqs), rot_dim, layout, mscale)
         self._ref = ctypes.byref(self._args)
         self._keep = freqs
 
@@ -209,7 +209,7 @@ _DATA_PTR, _GET_DEVICE = operator.methodcaller("data_ptr"), operator.methodcalle
 
 
 def _on_one_device(*xs) -> list:
-    """The addresses of device buffers; tensors among them must lie on one CUDA device."""
+    """The addresses of device buffers; tensors among them must lie on one CUDA device (numpy arrays never do)."""
     try:                                       # all tensors: the common case of a step's call
         found = set(map(_GET_DEVICE, xs))
         if len(found) == 1 and found.pop() >= 0:
@@ -225,6 +225,8 @@ def _on_one_device(*xs) -> list:
             d = x.get_device()
             p = x.data_ptr()
         except AttributeError:                 # an address
+            if isinstance(x, np.ndarray):
+                raise RmError(RM_E_INVAL, "a numpy array is not device memory")
             found.append(_ptr(x))
             continue
         if d != dev:
@@ -516,7 +518,9 @@ class ops:
     def qk_norm_rope(qkv, qkv_stride, q_out, q_stride, k_out, k_stride, T, n_q_heads, n_kv_heads, head_dim,
                      q_gain, k_gain, eps, rope, positions, cache=None, slots=None, stream=None):
         """rope: Rope or None; cache: KvCache or None; k_out may be None."""
-        x, qo, ko, gq, gk, pos, sl = _on_one_device(qkv, q_out, k_out, q_gain, k_gain, positions, slots)
+        x, qo, ko, gq, gk, pos, sl, _, _ = _on_one_device(
+            qkv, q_out, k_out, q_gain, k_gain, positions, slots, None if cache is None else cache._keep[0],
+            None if rope is None else rope._keep)
         _check(lib().rm_op_qk_norm_rope(x, qkv_stride, qo, q_stride, ko, k_stride, T, n_q_heads, n_kv_heads,
                                         head_dim, gq, gk, eps, None if rope is None else rope._ref, pos,
                                         None if cache is None else cache._ref, sl, _stream(stream)))
@@ -542,7 +546,7 @@ class ops:
         """workspace: device buffer of attn_decode_workspace(...) bytes (its size is read from a tensor)."""
         if workspace_bytes is None:
             workspace_bytes = workspace.numel() * workspace.element_size()
-        q, tab, ln, o, ws = _on_one_device(q, block_table, length, out, workspace)
+        q, tab, ln, o, ws, _ = _on_one_device(q, block_table, length, out, workspace, cache._keep[0])
         _check(lib().rm_op_attn_decode(q, q_stride, cache._ref, tab, table_stride, ln, n_seqs, n_q_heads, window,
                                        sinks, o, out_stride, ws, workspace_bytes, _stream(stream)))
 

@@ -171,6 +171,40 @@ def test_without_a_device_the_calls_say_so():
         refused(call, rm.RM_E_DEVICE)
 
 
+class Buffer:
+    """What the binding asks of a tensor: its device (-1: host) and its address."""
+
+    def __init__(self, device):
+        self.device = device
+
+    def get_device(self):
+        return self.device
+
+    def data_ptr(self):
+        return A
+
+
+@pytest.mark.parametrize("call", [
+    lambda x: rm.KvCache(Buffer(1), x, n_pages=4, page_size=16, n_kv_heads=1, head_dim=64),
+    lambda x: rm.ops.kv_slots(**{**SLOTS, "offsets": Buffer(1), "free_pages": x}),
+    lambda x: rm.ops.attn_window(**{**WINDOW, "out": Buffer(1), "offsets_dev": x}),
+    lambda x: rm.ops.attn_decode(**{**DECODE, "q": Buffer(1), "length": x, "cache": cache()}),
+    lambda x: rm.ops.qk_norm_rope(**{**ROPE, "qkv": Buffer(1), "positions": x}, rope=rm.Rope(A, 64), cache=cache())])
+@pytest.mark.parametrize("where", ["host", "numpy", "another device"])
+def test_buffers_that_are_not_on_the_calls_device_are_refused(call, where):
+    x = {"host": Buffer(-1), "numpy": np.zeros(64), "another device": Buffer(0)}[where]
+    refused(lambda: call(x))
+
+
+def test_a_cache_or_rotation_of_another_device_is_refused():
+    for host in (Buffer(-1), np.zeros(32)):
+        refused(lambda: rm.Rope(host, 64))
+    other = cache(k=Buffer(0), v=Buffer(0))
+    refused(lambda: rm.ops.attn_decode(**{**DECODE, "q": Buffer(1), "cache": other}))
+    refused(lambda: rm.ops.qk_norm_rope(**{**ROPE, "qkv": Buffer(1)}, rope=rm.Rope(A, 64), cache=other))
+    refused(lambda: rm.ops.qk_norm_rope(**{**ROPE, "qkv": Buffer(1)}, rope=rm.Rope(Buffer(0), 64), cache=cache()))
+
+
 def test_struct_layouts_match_the_header():
     assert ctypes.sizeof(rm.KvCache(A, A, n_pages=1, page_size=1, n_kv_heads=1, head_dim=8)._args) == 64
     assert ctypes.sizeof(rm.Rope(A, 2)._args) == 24

@@ -674,6 +674,12 @@ def test_attn_decode_scores_of_minus_infinity(d, L, first):
         assert np.all(np.abs(f64(out) - ref) <= attention_bound(ref, mag, top))
 
 
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (0, 2 ** 31 - 1), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2 ** 31 - 1)])
+def test_attention_of_the_largest_windows_and_sinks(window, sinks):
+    window_case([1, 300, 129], 4, 2, 64, window, sinks)
+    decode_case([1, 300, 129, 0], 4, 2, 64, 16, window, sinks)
+
+
 def test_offsets_beyond_32_bits():
     # a cache of over 2^32 elements: pages at its two ends, written through slots and read back
     hkv, d, page = 8, 128, 16
