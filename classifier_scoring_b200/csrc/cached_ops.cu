@@ -202,10 +202,9 @@ int rm_op_attn_window(const void* q, int64_t q_stride, const void* k, int64_t k_
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out))
     return set_error(RM_E_INVAL, "q, k, v and out must be 16-byte aligned");
   if (T == 0) return RM_OK;
-  int sms = 0;
-  RM_CHECK(check_on_device(out, &sms));
+  RM_CHECK(check_on_device(out));
   RM_LAUNCH(attn_window_launch(q, q_stride, k, k_stride, v, v_stride, offsets, n_seqs, T, n_q_heads,
-                               n_kv_heads, head_dim, window, sinks, out, out_stride, sms,
+                               n_kv_heads, head_dim, window, sinks, out, out_stride,
                                static_cast<cudaStream_t>(stream)));
   return RM_OK;
 }

@@ -182,7 +182,7 @@ cudaError_t qk_norm_rope_launch(const void* qkv, int64_t qkv_stride, void* q_out
 cudaError_t attn_window_launch(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                const void* v, int64_t v_stride, const int32_t* offsets, int n,
                                int T, int hq, int hkv, int d, int window, int sinks, void* out,
-                               int64_t out_stride, int num_sms, cudaStream_t st);
+                               int64_t out_stride, cudaStream_t st);
 size_t attn_decode_workspace(int n, int hq, const rm_kv_cache& cache);
 cudaError_t attn_decode_launch(const void* q, int64_t q_stride, const rm_kv_cache& cache,
                                const int32_t* table, int table_stride, const int32_t* length,
