@@ -38,6 +38,14 @@ struct PageDiv {
     return q + (x - q * P > 0);
   }
 };
+PageDiv page_div(int page_size) {
+  PageDiv div;
+  div.P = page_size;
+  div.shift = 31;
+  while ((1 << (div.shift - 31)) < page_size) ++div.shift;
+  div.mul = static_cast<uint32_t>(((1ull << div.shift) + page_size - 1) / page_size);
+  return div;
+}
 
 __global__ void __launch_bounds__(1024, 1)
     kv_slots_kernel(const int32_t* len_before, const int32_t* n_new, int n, PageDiv div,
@@ -231,7 +239,7 @@ struct RopeArgs {
   const int32_t* positions;
   void *kc, *vc;
   int64_t page_stride, n_slots;
-  int page_size;
+  PageDiv div;
   const float *k_scale, *v_scale;
   const int64_t* slots;
   int parts, per_part;                        // warps per token, heads per warp
@@ -256,9 +264,10 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<LP>::kBlocks) qk_no
   __shared__ __align__(16) float swap[kRopeWarps][32 * 8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kRopeWarps + warp;
-  const int t = static_cast<int>(item / a.parts), part = static_cast<int>(item % a.parts);
-  if (t >= a.T) return;
+  // a CTA's warps take tokens, or runs of one token's heads
+  const int t = a.parts == 1 ? static_cast<int>(blockIdx.x) * kRopeWarps + warp : static_cast<int>(blockIdx.x);
+  const int part = a.parts == 1 ? 0 : static_cast<int>(blockIdx.y) * kRopeWarps + warp;
+  if (t >= a.T || part >= a.parts) return;
   constexpr int kPer = 32 / LP;               // heads a warp holds at once
   const int c = lane % LP, sub = lane / LP;   // this lane's dims 8c..8c+7 of its head
   const bool live = 8 * c < a.d;
@@ -317,8 +326,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<LP>::kBlocks) qk_no
   if (a.kc != nullptr) {
     const int64_t slot = a.slots[t];
     if (slot >= 0 && slot < a.n_slots) {
-      const int64_t page = slot / a.page_size;
-      cache_row = page * a.page_stride + (slot - page * a.page_size) * a.d;
+      const int64_t page = slot <= 0x7fffffff ? a.div.floor(static_cast<int>(slot)) : slot / a.div.P;
+      cache_row = page * a.page_stride + (slot - page * a.div.P) * a.d;
     }
   }
   // the partner dims of an 8-dim chunk under RM_ROPE_HALF
@@ -345,7 +354,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<LP>::kBlocks) qk_no
       gain[2] = f32x2_pack(g1.x, g1.y);
       gain[3] = f32x2_pack(g1.z, g1.w);
     }
-    const int cache_head = a.page_size * a.d;
+    const int cache_head = a.div.P * a.d;
     int own = ha + sub - first;               // this lane's head among its kind
     bf16* dst = out == nullptr ? nullptr : out + static_cast<int64_t>(own) * a.d + 8 * c;
     E* cdst = cache == nullptr ? nullptr : cache + cache_row + static_cast<int64_t>(own) * cache_head + 8 * c;
@@ -450,10 +459,10 @@ template <typename E, int LP> cudaError_t rope_go(RopeArgs a, int num_sms, cudaS
   const int per = (steps + want - 1) / want;
   a.per_part = per * kPer;
   a.parts = (steps + per - 1) / per;
-  const int64_t ctas = (static_cast<int64_t>(a.T) * a.parts + kRopeWarps - 1) / kRopeWarps;
-  if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+  const dim3 grid = a.parts == 1 ? dim3((static_cast<unsigned>(a.T) + kRopeWarps - 1) / kRopeWarps)
+                                 : dim3(static_cast<unsigned>(a.T), (a.parts + kRopeWarps - 1) / kRopeWarps);
   PdlScope pdl(true);
-  return launch_k(qk_norm_rope_kernel<E, LP>, dim3(static_cast<unsigned>(ctas)), dim3(kRopeWarps * 32), 0, st, a);
+  return launch_k(qk_norm_rope_kernel<E, LP>, grid, dim3(kRopeWarps * 32), 0, st, a);
 }
 
 }  // namespace
@@ -469,11 +478,7 @@ cudaError_t kv_slots_launch(const int32_t* len_before, const int32_t* n_new, int
     const cudaError_t e = allow_smem(kv_slots_kernel, (3 * kMaxSlotSeqs + 2) * 4, allowed);
     if (e != cudaSuccess) return e;
   }
-  PageDiv div;
-  div.P = page_size;
-  div.shift = 31;
-  while ((1 << (div.shift - 31)) < page_size) ++div.shift;
-  div.mul = static_cast<uint32_t>(((1ull << div.shift) + page_size - 1) / page_size);
+  const PageDiv div = page_div(page_size);
   // One CTA for a step's few tokens; a run of tokens per thread over many CTAs
   // for prompts (251k tokens of 1000 requests: 25.8 us on one cluster of eight
   // CTAs); one cluster when the lengths advance in place.
@@ -535,7 +540,7 @@ cudaError_t qk_norm_rope_launch(const void* qkv, int64_t qkv_stride, void* q_out
   a.vc = cache.v;
   a.page_stride = cache.page_stride;
   a.n_slots = static_cast<int64_t>(cache.n_pages) * cache.page_size;
-  a.page_size = cache.page_size;
+  a.div = page_div(std::max(1, cache.page_size));
   a.k_scale = cache.k_scale;
   a.v_scale = cache.v_scale;
   a.slots = slots;
