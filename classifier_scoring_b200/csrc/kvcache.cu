@@ -220,6 +220,7 @@ constexpr int kRopeMaxDim = 256;
 template <int LP> struct RopeShape {
   static constexpr int kBatch = LP >= 16 ? 4 : 2;
   static constexpr int kBlocks = LP >= 16 ? 4 : 5;
+  static constexpr bool kSlotFirst = LP < 16;           // the slot's load over the trigonometry: long heads have no registers for it
 };
 
 struct RopeArgs {
@@ -268,6 +269,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<LP>::kBlocks) qk_no
   const int t = a.parts == 1 ? static_cast<int>(blockIdx.x) * kRopeWarps + warp : static_cast<int>(blockIdx.x);
   const int part = a.parts == 1 ? 0 : static_cast<int>(blockIdx.y) * kRopeWarps + warp;
   if (t >= a.T || part >= a.parts) return;
+  const int position = a.rot > 0 ? a.positions[t] : 0;
+  const int64_t early = RopeShape<LP>::kSlotFirst && a.kc != nullptr ? a.slots[t] : -1;
   constexpr int kPer = 32 / LP;               // heads a warp holds at once
   const int c = lane % LP, sub = lane / LP;   // this lane's dims 8c..8c+7 of its head
   const bool live = 8 * c < a.d;
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<LP>::kBlocks) qk_no
   const int half = a.rot / 2;
   uint64_t cs[4], sn[4];                      // of the lane's dims: y = x cs + partner sn
   if (half > 0) {
-    const double pos = a.positions[t];
+    const double pos = position;
     for (int i = lane; i < half; i += 32) {
       // whole turns leave the angle in 64 bits, before it is rounded to fp32
       const double turns = pos * a.freqs[i] * 0.15915494309189535;
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<LP>::kBlocks) qk_no
   }
   int64_t cache_row = -1;
   if (a.kc != nullptr) {
-    const int64_t slot = a.slots[t];
+    const int64_t slot = RopeShape<LP>::kSlotFirst ? early : a.slots[t];
     if (slot >= 0 && slot < a.n_slots) {
       const int64_t page = slot <= 0x7fffffff ? a.div.floor(static_cast<int>(slot)) : slot / a.div.P;
       cache_row = page * a.page_stride + (slot - page * a.div.P) * a.d;
