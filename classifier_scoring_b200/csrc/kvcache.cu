@@ -21,7 +21,11 @@ namespace {
 // used_after may be len_before and used_before: then all CTAs form one cluster
 // whose barrier separates the reads from the writes.
 // ---------------------------------------------------------------------------
+// Tokens a thread takes in a row: eight share a search, a page lookup and wide
+// stores (251k tokens of 1000 requests: 5.7 us); one where every thread has at
+// most one, whose lookups then do not wait for one another.
 constexpr int kSlotRun = 8;
+constexpr int kSlotSingles = 148 * 256;
 constexpr int kMaxSlotSeqs = 16384;
 
 // x / P = x * mul >> shift for 0 <= x < 2^31, P = 1..1024 (2^shift = 2^31 * the
@@ -47,6 +51,7 @@ PageDiv page_div(int page_size) {
   return div;
 }
 
+template <int kRun>
 __global__ void __launch_bounds__(1024, 1)
     kv_slots_kernel(const int32_t* len_before, const int32_t* n_new, int n, PageDiv div,
                     const int32_t* __restrict__ free_pages, int n_free, const int32_t* used_before,
@@ -142,15 +147,15 @@ __global__ void __launch_bounds__(1024, 1)
     const int i = upper_index(pg, m, g);
     block_table[static_cast<int64_t>(i) * stride + div.ceil(before[i]) + (g - pg[i])] = free_pages[used + g];
   }
-  // kSlotRun consecutive tokens a thread: one search for their request, one
+  // kRun consecutive tokens a thread: one search for their request, one
   // page lookup per page, wide stores
-  for (int64_t t = static_cast<int64_t>(at) * kSlotRun; t < T; t += static_cast<int64_t>(all) * kSlotRun) {
-    int64_t slot[kSlotRun];
-    int pos[kSlotRun];
+  for (int64_t t = static_cast<int64_t>(at) * kRun; t < T; t += static_cast<int64_t>(all) * kRun) {
+    int64_t slot[kRun];
+    int pos[kRun];
     int i = 0, p = 0, b = 0, rem = 0, page = 0, left = 0;      // left: tokens up to the request's end
     if (t < tokens) i = upper_index(off, m, t) - 1;
 #pragma unroll
-    for (int k = 0; k < kSlotRun; ++k) {
+    for (int k = 0; k < kRun; ++k) {
       if (t + k >= tokens) {
         slot[k] = -1;
         pos[k] = 0;
@@ -180,16 +185,16 @@ __global__ void __launch_bounds__(1024, 1)
       ++rem;
       --left;
     }
-    if (wide && t + kSlotRun <= T) {
+    if (kRun % 4 == 0 && wide && t + kRun <= T) {
 #pragma unroll
-      for (int k = 0; k < kSlotRun / 4; ++k)
+      for (int k = 0; k < kRun / 4; ++k)
         reinterpret_cast<int4*>(positions + t)[k] = make_int4(pos[4 * k], pos[4 * k + 1], pos[4 * k + 2], pos[4 * k + 3]);
 #pragma unroll
-      for (int k = 0; k < kSlotRun / 2; ++k)
+      for (int k = 0; k < kRun / 2; ++k)
         reinterpret_cast<longlong2*>(slots + t)[k] = make_longlong2(slot[2 * k], slot[2 * k + 1]);
     } else {
 #pragma unroll
-      for (int k = 0; k < kSlotRun; ++k)
+      for (int k = 0; k < kRun; ++k)
         if (t + k < T) {
           slots[t + k] = slot[k];
           positions[t + k] = pos[k];
@@ -468,24 +473,23 @@ template <typename E, int LP> cudaError_t rope_go(RopeArgs a, int num_sms, cudaS
   return launch_k(qk_norm_rope_kernel<E, LP>, grid, dim3(kRopeWarps * 32), 0, st, a);
 }
 
-}  // namespace
-
-cudaError_t kv_slots_launch(const int32_t* len_before, const int32_t* n_new, int n, int page_size,
-                            const int32_t* free_pages, int n_free, const int32_t* used_before,
-                            int32_t* block_table, int stride, int T, int32_t* offsets,
-                            int32_t* positions, int64_t* slots, int32_t* len_after,
-                            int32_t* used_after, int32_t* unserved, cudaStream_t st) {
+template <int kRun>
+cudaError_t slots_go(const int32_t* len_before, const int32_t* n_new, int n, int page_size,
+                     const int32_t* free_pages, int n_free, const int32_t* used_before,
+                     int32_t* block_table, int stride, int T, int32_t* offsets,
+                     int32_t* positions, int64_t* slots, int32_t* len_after,
+                     int32_t* used_after, int32_t* unserved, cudaStream_t st) {
   const size_t smem = (3 * static_cast<size_t>(n) + 2) * 4;
   if (smem > 48 * 1024) {
     static std::atomic<unsigned long long> allowed{0};
-    const cudaError_t e = allow_smem(kv_slots_kernel, (3 * kMaxSlotSeqs + 2) * 4, allowed);
+    const cudaError_t e = allow_smem(kv_slots_kernel<kRun>, (3 * kMaxSlotSeqs + 2) * 4, allowed);
     if (e != cudaSuccess) return e;
   }
   const PageDiv div = page_div(page_size);
   // One CTA for a step's few tokens; a run of tokens per thread over many CTAs
   // for prompts (251k tokens of 1000 requests: 25.8 us on one cluster of eight
   // CTAs); one cluster when the lengths advance in place.
-  const int64_t runs = (static_cast<int64_t>(T) + kSlotRun - 1) / kSlotRun;
+  const int64_t runs = (static_cast<int64_t>(T) + kRun - 1) / kRun;
   const bool in_place = len_after == len_before || used_after == used_before;
   const int threads = n > 4096 ? 1024 : 256;
   int ctas = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(148, (runs + threads - 1) / threads)));
@@ -504,9 +508,21 @@ cudaError_t kv_slots_launch(const int32_t* len_before, const int32_t* n_new, int
   cfg.attrs = attr;
   cfg.numAttrs = cluster ? 2 : 1;
   const bool wide = ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(slots)) & 15) == 0;
-  return cudaLaunchKernelEx(&cfg, kv_slots_kernel, len_before, n_new, n, div, free_pages, n_free,
+  return cudaLaunchKernelEx(&cfg, kv_slots_kernel<kRun>, len_before, n_new, n, div, free_pages, n_free,
                             used_before, block_table, stride, T, offsets, positions, slots,
                             len_after, used_after, unserved, wide, cluster);
+}
+
+}  // namespace
+
+cudaError_t kv_slots_launch(const int32_t* len_before, const int32_t* n_new, int n, int page_size,
+                            const int32_t* free_pages, int n_free, const int32_t* used_before,
+                            int32_t* block_table, int stride, int T, int32_t* offsets,
+                            int32_t* positions, int64_t* slots, int32_t* len_after,
+                            int32_t* used_after, int32_t* unserved, cudaStream_t st) {
+  auto go = T <= kSlotSingles ? slots_go<1> : slots_go<kSlotRun>;
+  return go(len_before, n_new, n, page_size, free_pages, n_free, used_before, block_table, stride, T, offsets,
+            positions, slots, len_after, used_after, unserved, st);
 }
 
 cudaError_t qk_norm_rope_launch(const void* qkv, int64_t qkv_stride, void* q_out, int64_t q_stride,
