@@ -96,7 +96,7 @@ def test_slots_of_the_most_sequences(in_place):
 
 
 @pytest.mark.parametrize("what", ["pages", "tokens", "row", "negative length", "negative count", "used", "used beyond", "no pages"])
-@pytest.mark.parametrize("n", [7, 700])
+@pytest.mark.parametrize("n", [7, 700, 3000])
 def test_slots_serve_what_fits_and_nothing_behind(what, n):
     before, new, free, table, T = slots_case(n, 1, 30, 50, 16, 3 * n)
     used, k = 2, n // 2
