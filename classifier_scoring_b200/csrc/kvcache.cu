@@ -14,7 +14,7 @@ namespace {
 
 // ---------------------------------------------------------------------------
 // Slot maps.  Bound by latency: a few dependent reads, a scan and the writes
-// (5.5 us for 64 requests, 5.7 us for 1000 requests of 251k tokens, 3 MB).
+// (2.9 us for a step of 64 requests, 5.7 us for 251k tokens of 1000, 3 MB).
 // Every CTA scans the n requests for itself (n is small beside the tokens, and
 // a scan costs less than handing its result on through memory), then the
 // tokens and new pages are shared out over all threads.  len_after and
@@ -230,8 +230,8 @@ __global__ void __launch_bounds__(1024, 1)
 // warps meet, and a head is read whole before it is written, so the outputs
 // may lie over the input.
 // Measured on B200, 25k tokens of 16 + 16 + 16 heads of 128, normed and
-// rotated into a bf16 cache: 141 us, 5.2 TB/s, 79% of a copy's rate (partners
-// through shared memory: 144 us).
+// rotated into a bf16 cache: 138 us, 5.3 TB/s, 80% of a copy's rate (partners
+// through shared memory: 3 us more).
 // ---------------------------------------------------------------------------
 constexpr int kRopeWarps = 4;
 constexpr int kRopeMaxDim = 256;
