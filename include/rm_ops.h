@@ -375,8 +375,9 @@ int rm_op_qk_norm_rope(const void* qkv, int64_t qkv_stride, void* q_out, int64_t
  * int32[n_seqs+1], offsets[0] = 0, non-decreasing (empty sequences allowed),
  * offsets[n_seqs] <= T (cut to it); rows behind it are not written.  Values
  * and keys that a row does not see do not reach it, infinities and NaN among
- * them; a row whose seen scores are all -infinity is NaN.  out overlaps no
- * input.  head_dim 64 or 128; pointers 16-byte aligned, strides multiples of 8
+ * them; a row whose seen scores are all -infinity is NaN.  Finite values are
+ * taken up to |v| * keys = 2^87 (the sums of p v are divided at the end, and p
+ * may reach 2^40 before its reference moves).  out overlaps no input.  head_dim 64 or 128; pointers 16-byte aligned, strides multiples of 8
  * elements; n_q_heads / n_kv_heads <= 128. */
 int rm_op_attn_window(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                       const void* v, int64_t v_stride, const int32_t* offsets, int32_t n_seqs,
@@ -393,8 +394,9 @@ int rm_op_attn_window(const void* q, int64_t q_stride, const void* k, int64_t k_
  * results go to workspace: device memory of rm_attn_decode_workspace bytes,
  * 16-byte aligned, overwritten, which no other call may use at the same time
  * (calls captured in graphs that may overlap need workspaces of their own).
- * Pages that a window hides are not read.  out overlaps no input.
- * cache->head_dim 64 or 128. */
+ * Pages that a window hides are not read.  Finite values are taken up to
+ * |v| * keys = 2^127 (the sums of p v are divided at the end).  out overlaps no
+ * input.  cache->head_dim 64 or 128. */
 int rm_op_attn_decode(const void* q, int64_t q_stride, const rm_kv_cache* cache,
                       const int32_t* block_table, int32_t table_stride, const int32_t* length,
                       int32_t n_seqs, int32_t n_q_heads, int32_t window, int32_t sinks, void* out,

@@ -441,6 +441,27 @@ def test_attn_window_scores_that_climb():
     assert np.all(np.abs(f64(out).reshape(T, 1, d) - ref) <= attention_bound(ref, mag, top))
 
 
+def test_attention_of_large_values():
+    # values near the documented bounds, the window's under scores that climb
+    T, d = 700, 128
+    q = torch.ones(T, d, dtype=torch.bfloat16, device="cuda")
+    k = (torch.arange(T, device="cuda")[:, None] * torch.ones(d, device="cuda") * 0.02).to(torch.bfloat16)
+    v = (randn((T, d), 3) * 2.0 ** 70).to(torch.bfloat16)
+    out = torch.empty_like(v)
+    rm.ops.attn_window(q, d, k, d, v, d, dev([0, T], torch.int32), 1, T, 1, 1, d, 0, 0, out, d)
+    torch.cuda.synchronize()
+    x = [f64(t).reshape(T, 1, d) for t in (q, k, v)]
+    ref, mag, top = C.attend_window(*x, [0, T], 0, 0)
+    assert np.all(np.abs(f64(out).reshape(T, 1, d) - ref) <= attention_bound(ref, mag, top))
+    v = (v.float() * 2.0 ** 40).to(torch.bfloat16)
+    cache, _, _, table = paged([k[:, None]], [v[:, None]], 16, 4)
+    space = torch.empty(rm.ops.attn_decode_workspace(1, 1, cache), dtype=torch.uint8, device="cuda")
+    rm.ops.attn_decode(q[:1] * 0.01, d, cache, dev(table, torch.int32), table.shape[1], dev([T], torch.int32), 1, 1, 0, 0, out, d, space)
+    torch.cuda.synchronize()
+    ref, mag, top = C.attend(f64(q[:1] * 0.01), f64(k)[:, None], f64(v)[:, None], np.arange(T))
+    assert np.all(np.abs(f64(out[:1]) - ref) <= attention_bound(ref, mag, top))
+
+
 @pytest.mark.parametrize("bad", [NAN, float("inf"), -float("inf")])
 @pytest.mark.parametrize("where", ["k", "v"])
 @pytest.mark.parametrize("d", [64, 128])
