@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t qd = smem_desc_k_sw128(sbase + SL::kQ + x * SL::kBuf);
       int slot = 0;                        // of the chunk's K; its V lies in the next one
       uint32_t turn = 0;                   // parity of that slot's full barrier
-      uint32_t q_turn = 0, p_turn[2] = {0, 0}, s_turn = 0, o_turn = 0;
+      uint32_t q_turn = 0, p_turn = 0, s_turn = 0, o_turn = 0;
       uint32_t pipe_turn = x ^ 1;          // tile 0 begins
       // the previous chunk's P V, if there is one still to be issued, and its V
       bool todo = false, opens = false, closes = false, ok = true;
@@ -526,9 +526,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t v = smem_desc_v(sbase + SL::kKv + v_slot * SL::kBuf);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {                     // P comes 64 keys at a time
-          if (v_steps <= half * 4) continue;
-          if (!(ok = wait_warp(p_full(x, half), p_turn[half]))) return;
-          p_turn[half] ^= 1;
+          // (for a half without keys too: its warps have then seen this
+          // chunk's S, whose barrier may go on to the next)
+          if (!(ok = wait_warp(p_full(x, half), p_turn))) return;
           tc_fence_after();
           if (v_steps >= half * 4 + 4) {
 #pragma unroll
@@ -540,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_ts(lead, d_o, d_s + half * 64 + (k & 3) * 8, v + 128ull * k, idesc_o, !opens || k > 0);
           }
         }
+        p_turn ^= 1;
         if (closes) {
           commit(lead, o_full(x));
           o_turn ^= 1;
@@ -759,10 +760,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_16cols(ts + y * 16, pk);     // over scores that are read
           }
           tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_full(x, half));
         }
+        // Without keys as well: S's barrier is waited for by parity, so it must
+        // not complete again before every warp of the tile has passed it.
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(x, half));
         l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
         // Has a maximum left its reference behind?  By up to 2^kLate the sums
         // take it (P and O have the exponents of fp32), and the next chunk moves

@@ -383,6 +383,15 @@ def test_attn_window_of_many_items(n, lo, hi, hq, hkv, d, window, sinks):
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
 
 
+@pytest.mark.parametrize("n,lo,hi,hq,hkv,d,window,sinks", [
+    (700, 1, 16, 8, 8, 64, 0, 0), (90, 129, 192, 6, 6, 64, 0, 0), (60, 200, 500, 4, 4, 128, 64, 1), (50, 300, 400, 12, 3, 64, 100, 64),
+    (500, 1, 64, 16, 2, 128, 0, 0), (30, 600, 800, 8, 8, 64, 16, 16)])
+def test_attn_window_chunks_of_few_keys(n, lo, hi, hq, hkv, d, window, sinks):
+    # chunks of at most 64 keys (short sequences, ends, sinks) leave half of the softmax without keys: its warps keep
+    # the tile's turns all the same
+    test_attn_window_of_many_items(n, lo, hi, hq, hkv, d, window, sinks)
+
+
 def test_attn_window_captured_replayed_and_on_two_streams():
     # a captured call on buffers that change, and two calls at once on streams of their own
     lens, hq, hkv, d = [200, 1, 77, 300], 8, 4, 128
