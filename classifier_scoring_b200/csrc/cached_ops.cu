@@ -158,6 +158,8 @@ int rm_op_qk_norm_rope(const void* qkv, int64_t qkv_stride, void* q_out, int64_t
     return set_error(RM_E_INVAL, "qkv, q_out and k_out must be 16-byte aligned");
   if ((q_gain == nullptr) != (k_gain == nullptr))
     return set_error(RM_E_INVAL, "q_gain and k_gain go together");
+  if (((reinterpret_cast<uintptr_t>(q_gain) | reinterpret_cast<uintptr_t>(k_gain)) & 3) != 0)
+    return set_error(RM_E_INVAL, "q_gain and k_gain must be 4-byte aligned");
   if (q_gain != nullptr && !(eps >= 0.f)) return set_error(RM_E_INVAL, "eps must be >= 0");
   rm_rope r = {};
   if (rope != nullptr) {

@@ -252,6 +252,7 @@ struct RopeArgs {
   int64_t k_stride;
   int T, hq, hkv, d, heads;                   // heads: those the call has to look at
   const float *q_gain, *k_gain;
+  bool wide_gains;                            // both 16-byte aligned
   float eps, inv_d;
   const double* freqs;
   int rot, interleaved;
@@ -370,12 +371,17 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<LP>::kBlocks) qk_no
     const bool norm = !kValue && gain_at != nullptr;
     uint64_t gain[4];
     if (norm && live) {
-      const float4 g0 = reinterpret_cast<const float4*>(gain_at + 8 * c)[0];
-      const float4 g1 = reinterpret_cast<const float4*>(gain_at + 8 * c)[1];
-      gain[0] = f32x2_pack(g0.x, g0.y);
-      gain[1] = f32x2_pack(g0.z, g0.w);
-      gain[2] = f32x2_pack(g1.x, g1.y);
-      gain[3] = f32x2_pack(g1.z, g1.w);
+      if (a.wide_gains) {
+        const float4 g0 = reinterpret_cast<const float4*>(gain_at + 8 * c)[0];
+        const float4 g1 = reinterpret_cast<const float4*>(gain_at + 8 * c)[1];
+        gain[0] = f32x2_pack(g0.x, g0.y);
+        gain[1] = f32x2_pack(g0.z, g0.w);
+        gain[2] = f32x2_pack(g1.x, g1.y);
+        gain[3] = f32x2_pack(g1.z, g1.w);
+      } else {                                // a slice of a packed parameter buffer
+#pragma unroll
+        for (int e = 0; e < 4; ++e) gain[e] = f32x2_pack(gain_at[8 * c + 2 * e], gain_at[8 * c + 2 * e + 1]);
+      }
     }
     const int cache_head = a.div.P * a.d;
     int own = ha + sub - first;               // this lane's head among its kind
@@ -561,6 +567,7 @@ cudaError_t qk_norm_rope_launch(const void* qkv, int64_t qkv_stride, void* q_out
   a.heads = cache.k != nullptr ? hq + 2 * hkv : (k_out != nullptr ? hq + hkv : hq);
   a.q_gain = q_gain;
   a.k_gain = k_gain;
+  a.wide_gains = ((reinterpret_cast<uintptr_t>(q_gain) | reinterpret_cast<uintptr_t>(k_gain)) & 15) == 0;
   a.eps = eps;
   a.inv_d = 1.f / static_cast<float>(d);
   a.freqs = rope.freqs;

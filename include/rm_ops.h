@@ -346,8 +346,9 @@ int rm_op_kv_slots(const int32_t* len_before, const int32_t* n_new, int32_t n_se
 /* Norm and rotation of a projection's queries and keys, and the cache write,
  * in one pass.  Row t of qkv holds the token's query heads, then its key
  * heads, then its value heads, head_dim elements each (bf16).  Per head:
- *   y = x / sqrt(mean(x^2) + eps) * gain      (q_gain, k_gain: fp32 [head_dim];
- *                                              both NULL = no norm)
+ *   y = x / sqrt(mean(x^2) + eps) * gain      (q_gain, k_gain: fp32 [head_dim],
+ *                                              4-byte aligned; both NULL =
+ *                                              no norm)
  *   z = y with its first rot_dim dims rotated by positions[t] (rope NULL: z = y)
  * in fp32, angles reduced in 64 bits (exact to fp32 rounding for any int32
  * position), rounded once.  Written: q_out (row t's query heads), k_out (its

@@ -125,6 +125,11 @@ def test_qk_norm_rope_refuses(kw):
     refused(lambda: rm.ops.qk_norm_rope(**{**ROPE, "rope": rm.Rope(A, 64), "cache": cache(), **kw}))
 
 
+@pytest.mark.parametrize("kw", [dict(q_gain=A + 2), dict(k_gain=A + 1), dict(q_gain=A + 6, k_gain=A + 4)])
+def test_qk_norm_rope_refuses_gains_that_no_float_lies_at(kw):
+    refused(lambda: rm.ops.qk_norm_rope(**{**ROPE, "rope": rm.Rope(A, 64), "cache": cache(), **kw}))
+
+
 WINDOW = dict(q=A, q_stride=128, k=A, k_stride=128, v=A, v_stride=128, offsets_dev=A, n_seqs=1, T=5, n_q_heads=2,
               n_kv_heads=2, head_dim=64, window=0, sinks=0, out=A, out_stride=128)
 

@@ -232,6 +232,27 @@ def test_qk_norm_rope_in_place_and_strides(in_place, pad, d, rot, layout):
     rope_case(50, 6, 3, d, rot, layout, True, "bf16", in_place=in_place, pad=pad, seed=pad)
 
 
+@pytest.mark.parametrize("d", [24, 64, 128, 256])
+@pytest.mark.parametrize("q_at,k_at", [(0, 1), (1, 0), (2, 3), (3, 5), (4, 8)])
+def test_qk_norm_rope_gains_anywhere_in_a_parameter_buffer(d, q_at, k_at):
+    # gains are fp32 slices of a packed buffer, at any element of it
+    T, hq, hkv = 13, 4, 2
+    flat = 1 + 0.2 * torch.randn(2 * d + 32, generator=torch.Generator().manual_seed(d)).cuda()
+    gq, gk = flat[q_at:q_at + d], flat[d + 8 + k_at:2 * d + 8 + k_at]
+    qkv = randn((T, (hq + 2 * hkv) * d), 2)
+    outs = []
+    for g in ((gq, gk), (gq.clone(), gk.clone())):
+        q, k = (torch.full((T, h * d), NAN, dtype=torch.bfloat16, device="cuda") for h in (hq, hkv))
+        rm.ops.qk_norm_rope(qkv, (hq + 2 * hkv) * d, q, hq * d, k, hkv * d, T, hq, hkv, d, *g, 1e-6, None, None)
+        outs.append((q, k))
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    x = f64(qkv).reshape(T, -1, d)
+    for got, rows, g, h in ((outs[0][0], x[:, :hq], gq, hq), (outs[0][1], x[:, hq:hq + hkv], gk, hkv)):
+        ref, mag = C.norm_rope(rows, f64(g), 1e-6, None, None, 0)
+        assert np.all(np.abs(f64(got).reshape(T, h, d) - ref) <= HALF_BF16 * np.abs(ref) + 2 * F32_RTOL * mag)
+
+
 def test_qk_norm_rope_far_positions():
     rope_case(64, 4, 2, 128, 128, 0, False, "bf16", far=2 ** 31 - 2, seed=4)
 
