@@ -172,6 +172,8 @@ def lib() -> ctypes.CDLL:
         "rm_op_res_ln": (ctypes.c_int, [P, P, P, P, P, I32, I32, F, I32, I32, P]),
         "rm_op_head": (ctypes.c_int, [P, P, I32, P, F, I32, I32, P, P]),
         "rm_arena_plan": (ctypes.c_int, [cfgp, I32, I32, I64, P, P, P, P, I32, P]),
+        "rm_op_timeouts": (ctypes.c_int, [P]),
+        "rm_selftest_op_wait": (ctypes.c_int, [I64]),
         "rm_rope_freqs": (ctypes.c_int, [I32, D, I32, D, D, D, D, P]),
         "rm_op_kv_slots": (ctypes.c_int, [P, P, I32, I32, P, I32, P, P, I32, I32, P, P, P, P, P, P, P]),
         "rm_op_qk_norm_rope": (ctypes.c_int, [P, I64, P, I64, P, I64, I32, I32, I32, I32, P, P, F, ropep, P,
@@ -604,6 +606,13 @@ def bounds_errors() -> int:
     return int(out[0])
 
 
+def op_timeouts() -> int:
+    """rm_op_timeouts: waits given up in kernels of ops calls on the current device since the last call (0 normally)."""
+    out = np.zeros(1, dtype=np.int64)
+    _check(lib().rm_op_timeouts(out.ctypes.data))
+    return int(out[0])
+
+
 def debug_fail_alloc(k: int) -> None:
     """rm_debug_fail_alloc: the k-th library allocation from now on fails (0 disarms)."""
     _check(lib().rm_debug_fail_alloc(int(k)))
@@ -615,3 +624,8 @@ def selftest_bounded_wait(limit_ns: int):
     ns = ctypes.c_int64()
     _check(lib().rm_selftest_bounded_wait(int(limit_ns), ctypes.byref(flag), ctypes.byref(ns)))
     return int(flag.value), int(ns.value)
+
+
+def selftest_op_wait(limit_ns: int) -> None:
+    """rm_selftest_op_wait: a wait of an op's kernel that nothing ends; op_timeouts then counts it."""
+    _check(lib().rm_selftest_op_wait(int(limit_ns)))

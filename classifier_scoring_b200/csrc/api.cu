@@ -1175,6 +1175,26 @@ void rm_destroy(rm_handle* h) {
 // rm_ops.h
 // ---------------------------------------------------------------------------
 
+int rm_op_timeouts(int64_t* out) {
+  if (out == nullptr) return set_error(RM_E_INVAL, "NULL argument");
+  int32_t words[ERR_WORDS], window = 0;
+  const int32_t zero[ERR_WORDS] = {};
+  RM_CUDA(cudaDeviceSynchronize());
+  RM_CUDA(cudaMemcpyFromSymbol(words, g_err_sink, sizeof words));
+  RM_CUDA(cudaMemcpyToSymbol(g_err_sink, zero, sizeof zero));
+  RM_CUDA(window_timeouts(&window));
+  *out = static_cast<int64_t>(words[ERR_TIMEOUT]) + window;
+  return RM_OK;
+}
+
+int rm_selftest_op_wait(int64_t limit_ns) {
+  if (limit_ns < 1000 || limit_ns > 10000000000LL)
+    return set_error(RM_E_INVAL, "limit_ns must be in 1e3 .. 1e10");
+  RM_CUDA(window_wait_selftest(static_cast<unsigned long long>(limit_ns), nullptr));
+  RM_CUDA(cudaDeviceSynchronize());
+  return RM_OK;
+}
+
 int rm_varlen_meta(const int32_t* offsets, int32_t n, int32_t n_heads, int32_t* rb_off,
                    int64_t* s_off) {
   if (offsets == nullptr || rb_off == nullptr || s_off == nullptr || n < 0 || n_heads < 1)

@@ -53,8 +53,8 @@
 // tile whose chunks hold such a V row that not every row sees, is computed
 // again from the keys it sees alone (attend_row.cuh).
 //
-// Every wait is bounded; one that gives up counts into the error word, and its
-// role stops.
+// Every wait is bounded; one that gives up counts into the error word that
+// rm_op_timeouts reads, and its role stops.
 //
 // Measured on B200: five documents of up to 32761 tokens, 32 heads on 8 of 128
 // dims, window 4096: 2.05 ms, 1.0 PFLOP/s of seen pairs (bound by a chunk's
@@ -187,8 +187,8 @@ __device__ __forceinline__ int warp_upper_index(const int32_t* a, int n, int key
   return lo;
 }
 
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
-  if (mbar_wait_for(bar, parity, kLimitNs)) return true;
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, unsigned long long limit_ns = kLimitNs) {
+  if (mbar_wait_for(bar, parity, limit_ns)) return true;
   atomicAdd(&g_window_err[ERR_TIMEOUT], 1);
   return false;
 }
@@ -891,6 +891,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// One thread waits, through this file's wait, on an mbarrier that nothing completes.
+__global__ void window_wait_selftest_kernel(unsigned long long limit_ns) {
+  __shared__ __align__(8) uint64_t bar;
+  if (threadIdx.x != 0) return;
+  mbar_init(smem_u32(&bar), 1);
+  mbar_init_fence();
+  wait(smem_u32(&bar), 0, limit_ns);
+}
+
 template <int D>
 cudaError_t launch(const WindowArgs& a, int T, int grid, cudaStream_t st) {
   CUtensorMap tq, tk, tv, to;
@@ -909,6 +918,20 @@ cudaError_t launch(const WindowArgs& a, int T, int grid, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t window_wait_selftest(unsigned long long limit_ns, cudaStream_t st) {
+  window_wait_selftest_kernel<<<1, 32, 0, st>>>(limit_ns);
+  return cudaGetLastError();
+}
+
+cudaError_t window_timeouts(int32_t* out) {
+  int32_t words[ERR_WORDS];
+  const int32_t zero[ERR_WORDS] = {};
+  cudaError_t e = cudaMemcpyFromSymbol(words, g_window_err, sizeof words);
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_window_err, zero, sizeof zero);
+  if (e == cudaSuccess) *out = words[ERR_TIMEOUT];
+  return e;
+}
 
 cudaError_t attn_window_launch(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                const void* v, int64_t v_stride, const int32_t* offsets, int n,

@@ -183,6 +183,10 @@ cudaError_t attn_window_launch(const void* q, int64_t q_stride, const void* k, i
                                const void* v, int64_t v_stride, const int32_t* offsets, int n,
                                int T, int hq, int hkv, int d, int window, int sinks, void* out,
                                int64_t out_stride, cudaStream_t st);
+// Waits of the windowed attention that gave up on the current device since the
+// last call; and one thread whose wait, by the given limit, is one of them.
+cudaError_t window_timeouts(int32_t* out);
+cudaError_t window_wait_selftest(unsigned long long limit_ns, cudaStream_t st);
 size_t attn_decode_workspace(int n, int hq, const rm_kv_cache& cache);
 cudaError_t attn_decode_launch(const void* q, int64_t q_stride, const rm_kv_cache& cache,
                                const int32_t* table, int table_stride, const int32_t* length,

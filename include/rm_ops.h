@@ -32,6 +32,19 @@
 extern "C" {
 #endif
 
+/* Failure detection of the calls below, which have no handle: waits for the
+ * current device, writes how many pipeline waits gave up in the kernels that
+ * rm_op_* calls of this process launched there since the last call (0 in normal
+ * operation; a kernel that gave one up returned early and its outputs are
+ * invalid), and clears the count.  out: host int64.  RM_E_INVAL for NULL,
+ * RM_E_CUDA on a CUDA error. */
+int rm_op_timeouts(int64_t* out);
+/* Failure detection without a fault, as rm_selftest_bounded_wait (rm.h): one
+ * thread waits on a barrier that nothing completes, through the wait of
+ * rm_op_attn_window, and gives up after limit_ns (1e3 .. 1e10), which the next
+ * rm_op_timeouts reports.  Synchronous; the CUDA context stays usable. */
+int rm_selftest_op_wait(int64_t limit_ns);
+
 /* Host helper: rb_off[n+1] and s_off[n+1] for the layout above (host arrays).
  * Returns RM_OK, RM_E_INVAL for a length < 1 or non-monotone offsets. */
 int rm_varlen_meta(const int32_t* offsets, int32_t n, int32_t n_heads,
@@ -160,7 +173,7 @@ int rm_op_attn_fused(const void* qkv, void* ctx, const int32_t* offsets, const i
  * [T][H]; offsets: DEVICE int32[n+1] with offsets[n] = T (host value T);
  * max_len: a host bound on every L_i (it sizes the launch: CTAs take fewer
  * heads each when rows are long).  RM_E_INVAL for other head dims or sizes < 1; waits that give up (none in
- * normal operation) count into an internal error word. */
+ * normal operation) are counted (rm_op_timeouts). */
 int rm_op_attn_tiles(const void* qkv, void* ctx, const int32_t* offsets, int32_t n_seqs, int32_t T,
                      int32_t n_heads, int32_t head_dim, int32_t max_len, int32_t causal,
                      void* stream);
@@ -185,7 +198,7 @@ int rm_attn_tc_tiles(const int32_t* offsets, int32_t n_seqs, int32_t* tiles);
  * DEVICE int32[n_seqs+1] with offsets[n_seqs] = T (host value T); tiles:
  * DEVICE int32[n_tiles+1] as rm_attn_tc_tiles wrote them for the same
  * offsets.  RM_E_INVAL for NULL pointers or sizes < 1; waits that give up
- * (none in normal operation) count into an internal error word. */
+ * (none in normal operation) are counted (rm_op_timeouts). */
 int rm_op_attn_tc(const void* qkv, void* ctx, const int32_t* offsets, const int32_t* tiles,
                   int32_t n_tiles, int32_t n_seqs, int32_t T, int32_t n_heads, int32_t causal,
                   void* stream);
@@ -210,8 +223,8 @@ int rm_attn_tcl_items(const int32_t* offsets, int32_t n_seqs, int32_t causal, in
  * int32[n_seqs+1] with offsets[n_seqs] = T (host value T); items: DEVICE
  * int32[n_items] as rm_attn_tcl_items wrote them for the same offsets and
  * causal flag.  RM_E_INVAL for NULL pointers, sizes < 1 or n_items >
- * 4 * n_seqs; waits that give up (none in normal operation) count into an
- * internal error word. */
+ * 4 * n_seqs; waits that give up (none in normal operation) are counted
+ * (rm_op_timeouts). */
 int rm_op_attn_tcl(const void* qkv, void* ctx, const int32_t* offsets, const int32_t* items,
                    int32_t n_items, int32_t n_seqs, int32_t T, int32_t n_heads, int32_t causal,
                    void* stream);
@@ -379,7 +392,8 @@ int rm_op_qk_norm_rope(const void* qkv, int64_t qkv_stride, void* q_out, int64_t
  * them; a row whose seen scores are all -infinity is NaN.  Finite values are
  * taken up to |v| * keys = 2^87 (the sums of p v are divided at the end, and p
  * may reach 2^40 before its reference moves).  out overlaps no input.  head_dim 64 or 128; pointers 16-byte aligned, strides multiples of 8
- * elements; n_q_heads / n_kv_heads <= 128. */
+ * elements; n_q_heads / n_kv_heads <= 128.  Waits that give up (none in normal
+ * operation) are counted (rm_op_timeouts); the outputs are then invalid. */
 int rm_op_attn_window(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                       const void* v, int64_t v_stride, const int32_t* offsets, int32_t n_seqs,
                       int32_t T, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,

@@ -176,6 +176,15 @@ def test_without_a_device_the_calls_say_so():
         refused(call, rm.RM_E_DEVICE)
 
 
+def test_timeouts_refuse_and_say_when_there_is_no_device():
+    import torch
+    assert rm.lib().rm_op_timeouts(None) == rm.RM_E_INVAL
+    for limit in (0, 999, 10 ** 10 + 1, -5):
+        refused(lambda: rm.selftest_op_wait(limit))
+    if not torch.cuda.is_available():
+        refused(rm.op_timeouts, rm.RM_E_CUDA)
+
+
 class Buffer:
     """What the binding asks of a tensor: its device (-1: host) and its address."""
 

@@ -753,6 +753,24 @@ def test_offsets_beyond_32_bits():
     assert np.all(np.abs(f64(out).reshape(hkv, d) - ref) <= attention_bound(ref, mag, top))
 
 
+# --- waits that give up ---------------------------------------------------------------------
+
+def test_a_wait_that_gives_up_is_counted_and_told_once():
+    # no kernel of the tests before gave one up; one that nothing ends is told, and the operators go on working
+    assert rm.op_timeouts() == 0
+    rm.selftest_op_wait(2_000_000)
+    rm.selftest_op_wait(2_000_000)
+    assert rm.op_timeouts() == 2
+    window_case([300, 20], 4, 2, 128, 100, 4)
+    assert rm.op_timeouts() == 0
+
+
+@pytest.fixture(scope="module", autouse=True)
+def no_wait_gives_up(cuda):
+    yield
+    assert rm.op_timeouts() == 0
+
+
 # --- what the device check refuses ---------------------------------------------------------
 
 def test_host_pointers_are_refused():
