@@ -58,7 +58,7 @@ template <int D, typename E, int NH> struct Shape {
 
 struct Parts {            // workspace
   float* o;               // [ctas][2][rows][D]
-  float* ml;              // [ctas][2][rows][2]
+  float* ml;              // [ctas][2][rows][2]: reference, sum
   int4* rec;              // [ctas]: unit that begins in the CTA's stretch and goes on behind it
 };
 
@@ -160,6 +160,17 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+// The reference of a row's exponentials, from its running maximum.  bf16 caches
+// take the maximum itself: the largest probability is then 1, which has no
+// rounding, and bf16 has the small ones.  fp16 (8-bit caches) runs out at
+// 2^-24, so there the largest is 2^15: weights down to 2^-32 of it keep the
+// precision of bf16, those below 2^-40 are 0 (with a largest of 1: 2^-17 and
+// 2^-25, and a long flat tail under one key was lost).  The sum and the output
+// carry the same factor.  From |maximum| = 2^20 on its fp32 step is 1/8 and the
+// subtraction would round, up to an overflow of fp16: the maximum itself.
+template <typename E> __device__ __forceinline__ float reference(float top) {
+  return sizeof(E) == 1 && fabsf(top) < 1048576.f ? top - 15.f : top;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
@@ -393,15 +404,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
         top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], w));
         top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], w));
       }
-      // The reference is the running maximum itself: the largest probability is
-      // then 1, which has no rounding.  It seldom moves, and only then is the
-      // output rescaled.
+      // The maximum seldom moves, and only then is the output rescaled.
       if (__any_sync(0xffffffffu, top[0] > m[nh][0] || top[1] > m[nh][1])) {
         float keep[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const float mn = fmaxf(m[nh][x], top[x]);
-          keep[x] = m[nh][x] == -INFINITY ? 0.f : ex2_approx_ftz(m[nh][x] - mn);
+          keep[x] = m[nh][x] == -INFINITY ? 0.f : ex2_approx_ftz(reference<E>(m[nh][x]) - reference<E>(mn));
           m[nh][x] = mn;
           l[nh][x] *= keep[x];
         }
@@ -410,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
 #pragma unroll
           for (int x = 0; x < 4; ++x) o[i][nh][x] *= keep[x & 1];
       }
-      const float ref[2] = {m[nh][0] == -INFINITY ? 0.f : m[nh][0], m[nh][1] == -INFINITY ? 0.f : m[nh][1]};
+      const float ref[2] = {m[nh][0] == -INFINITY ? 0.f : reference<E>(m[nh][0]),
+                            m[nh][1] == -INFINITY ? 0.f : reference<E>(m[nh][1])};
 #pragma unroll
       for (int kt = 0; kt < kKeys / 16; ++kt)
 #pragma unroll
@@ -467,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
+        m[nh][x] = reference<E>(m[nh][x]);                       // what the parts are joined by
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) l[nh][x] += __shfl_xor_sync(0xffffffffu, l[nh][x], w);
         if (g == 0) {
@@ -523,9 +534,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
         x1 += v.y;
       }
       if (whole) {
-        const float inv = lt == 0.f && mt == -INFINITY ? 0.f : vs / lt;       // no key: zeros
+        const float inv = lt == 0.f && mt == -INFINITY ? 0.f : 1.f / lt;      // no key: zeros
         *reinterpret_cast<uint32_t*>(a.out + s * a.out_stride + static_cast<int64_t>(h * group + r0 + r) * D + d2) =
-            pack_bf16x2(x0 * inv, x1 * inv);
+            pack_bf16x2(x0 * inv * vs, x1 * inv * vs);
       } else {
         *reinterpret_cast<float2*>(po + r * D + d2) = make_float2(x0, x1);
         if (d2 == 0) {
@@ -636,7 +647,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const De
     for (int i = 1; i < kGroups; ++i) acc += red[i][dim];
     const float vs = f8 && a.v_scale != nullptr ? a.v_scale[h] : 1.f;
     a.out[rec.x * a.out_stride + static_cast<int64_t>(h * group + r0 + r) * D + dim] =
-        __float2bfloat16_rn(lt == 0.f && mt == -INFINITY ? 0.f : acc * (vs / lt));
+        __float2bfloat16_rn(lt == 0.f && mt == -INFINITY ? 0.f : acc * (1.f / lt) * vs);
   }
 }
 

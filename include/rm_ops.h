@@ -409,7 +409,12 @@ int rm_op_attn_window(const void* q, int64_t q_stride, const void* k, int64_t k_
  * results go to workspace: device memory of rm_attn_decode_workspace bytes,
  * 16-byte aligned, overwritten, which no other call may use at the same time
  * (calls captured in graphs that may overlap need workspaces of their own).
- * Pages that a window hides are not read.  Finite values are taken up to
+ * Pages that a window hides are not read.  P is rounded to bf16 before the
+ * product with V as in rm_op_attn_window; over an e4m3 cache it is held in
+ * fp16, where weights down to 2^-32 of the largest that the same split of the
+ * row holds keep that precision and those below 2^-40 of it reach the sum
+ * only.  Queries over an e4m3 cache are held in fp16 too, relative to the
+ * largest of their head (entries below 2^-27 of it lose bits).  Finite values are taken up to
  * |v| * keys = 2^127 (the sums of p v are divided at the end).  out overlaps no
  * input.  cache->head_dim 64 or 128. */
 int rm_op_attn_decode(const void* q, int64_t q_stride, const rm_kv_cache* cache,

@@ -725,6 +725,31 @@ def test_attn_decode_scores_of_minus_infinity(d, L, first):
         assert np.all(np.abs(f64(out) - ref) <= attention_bound(ref, mag, top))
 
 
+@pytest.mark.parametrize("below", [18, 26, 30])
+@pytest.mark.parametrize("n,L,hq", [(1, 32, 1), (600, 1000, 1), (300, 500, 12)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attn_decode_8_bit_cache_of_a_dominant_key_and_a_flat_tail(d, n, L, hq, below):
+    # one key's weight is 2^below times each other's, and its value is 0: the output is the tail's share alone
+    k, v = torch.zeros(L, d, device="cuda"), randn((L, d), 5).float()
+    k[:, 0], k[0, 0], v[0] = -2.0, 16.0, 0.0
+    pages = -(-L // 16)
+    pools = [torch.full((pages * 16, d), 0x7f, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for pool, x in zip(pools, (k, v)):
+        pool[:L] = x.to(torch.float8_e4m3fn).view(torch.uint8)
+    cache = rm.KvCache(*pools, n_pages=pages, page_size=16, n_kv_heads=1, head_dim=d, dtype=rm.E4M3)
+    q = torch.zeros(n, hq, d, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = below * np.log(2) * d ** 0.5 / 18
+    out = torch.empty(n, hq * d, dtype=torch.bfloat16, device="cuda")
+    space = torch.empty(rm.ops.attn_decode_workspace(n, hq, cache), dtype=torch.uint8, device="cuda")
+    table = dev(np.tile(np.arange(pages), (n, 1)), torch.int32)
+    rm.ops.attn_decode(q, hq * d, cache, table, pages, dev([L] * n, torch.int32), n, hq, 0, 0, out, hq * d, space)
+    torch.cuda.synchronize()
+    held = [e4m3_pages(pool)[:L, None] for pool in pools]
+    ref, mag, top = C.attend(f64(q[0]), *held, np.arange(L))
+    err, bound = np.abs(f64(out).reshape(n, hq, d) - ref), attention_bound(ref, mag, top)
+    assert np.all(err <= bound), float((err / bound).max())
+
+
 @pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (0, 2 ** 31 - 1), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2 ** 31 - 1)])
 def test_attention_of_the_largest_windows_and_sinks(window, sinks):
     window_case([1, 300, 129], 4, 2, 64, window, sinks)
