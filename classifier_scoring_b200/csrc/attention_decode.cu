@@ -385,8 +385,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       }
     }
     // base-2 scores: elements 0, 1 of key 16 kt + g, 2, 3 of key 16 kt + 8 + g.
-    // Once a key is seen the reference is finite: scores of -inf weigh nothing,
-    // and a row of them alone ends as 0 / 0, unlike one that saw no key.
+    // Once a key is seen the maximum is above -inf: scores of -inf weigh nothing,
+    // and a row of them alone ends as 0 / 0.  So a maximum of -inf stands for no
+    // key seen, a sum of 0 and an output of 0; a NaN is in the output already.
     const float floor = keys != 0u ? -FLT_MAX : -INFINITY;
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
@@ -498,8 +499,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
             float mt = -INFINITY;
 #pragma unroll
             for (int k = 0; k < kWarps; ++k) mt = fmaxf(mt, ml[(k * kRows + r) * 2]);
-            float w = m[nh][x] == -INFINITY ? 0.f : ex2_approx_ftz(m[nh][x] - mt);
-            if (l[nh][x] != l[nh][x]) w = l[nh][x];              // a NaN seen before any maximum
+            const float w = m[nh][x] == -INFINITY ? 0.f : ex2_approx_ftz(m[nh][x] - mt);
             float* dst = sum + ((warp - i) * rows + r) * kPitch;
 #pragma unroll
             for (int dt = 0; dt < D / 16; ++dt)
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
         const float mk = ml[(k * kRows + r) * 2], lk = ml[(k * kRows + r) * 2 + 1];
-        lt += mk == -INFINITY ? lk : lk * ex2_approx_ftz(mk - mt);
+        lt += mk == -INFINITY ? 0.f : lk * ex2_approx_ftz(mk - mt);
       }
       float x0 = 0.f, x1 = 0.f;
       for (int k = 0; k < room; ++k) {
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
         x1 += v.y;
       }
       if (whole) {
-        const float inv = lt == 0.f && mt == -INFINITY ? 0.f : 1.f / lt;      // no key: zeros
+        const float inv = mt == -INFINITY ? 0.f : 1.f / lt;                   // no key: zeros
         *reinterpret_cast<uint32_t*>(a.out + s * a.out_stride + static_cast<int64_t>(h * group + r0 + r) * D + d2) =
             pack_bf16x2(x0 * inv * vs, x1 * inv * vs);
       } else {
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const De
   float lt = 0.f;
   for (int i = tid; i < parts; i += kJoinThreads) {
     const float* p = a.parts.ml + (slot(i) * kRows + r) * 2;
-    const float wi = p[0] == -INFINITY ? (p[1] != p[1] ? p[1] : 0.f) : ex2_approx_ftz(p[0] - mt);
+    const float wi = p[0] == -INFINITY ? 0.f : ex2_approx_ftz(p[0] - mt);
     w[i] = wi;
     lt += wi * p[1];
   }
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const De
     for (int i = 1; i < kGroups; ++i) acc += red[i][dim];
     const float vs = f8 && a.v_scale != nullptr ? a.v_scale[h] : 1.f;
     a.out[rec.x * a.out_stride + static_cast<int64_t>(h * group + r0 + r) * D + dim] =
-        __float2bfloat16_rn(lt == 0.f && mt == -INFINITY ? 0.f : acc * (1.f / lt) * vs);
+        __float2bfloat16_rn(mt == -INFINITY ? 0.f : acc * (1.f / lt) * vs);
   }
 }
 
