@@ -146,7 +146,7 @@ int rm_op_qk_norm_rope(const void* qkv, int64_t qkv_stride, void* q_out, int64_t
                        const float* k_gain, float eps, const rm_rope* rope,
                        const int32_t* positions, const rm_kv_cache* cache, const int64_t* slots,
                        void* stream) {
-  if (qkv == nullptr || q_out == nullptr) return set_error(RM_E_INVAL, "NULL argument");
+  if (T > 0 && (qkv == nullptr || q_out == nullptr)) return set_error(RM_E_INVAL, "NULL argument");
   if (T < 0 || !heads_ok(n_q_heads, n_kv_heads) || head_dim < 8 || head_dim % 8 != 0 || head_dim > 256)
     return set_error(RM_E_INVAL, "bad sizes");
   const int64_t d = head_dim;
@@ -167,14 +167,14 @@ int rm_op_qk_norm_rope(const void* qkv, int64_t qkv_stride, void* q_out, int64_t
     if (r.rot_dim < 0 || r.rot_dim % 2 != 0 || r.rot_dim > head_dim ||
         (r.layout != RM_ROPE_HALF && r.layout != RM_ROPE_INTERLEAVED))
       return set_error(RM_E_INVAL, "bad rotation");
-    if (r.rot_dim > 0 && (r.freqs == nullptr || positions == nullptr))
+    if (r.rot_dim > 0 && (r.freqs == nullptr || (T > 0 && positions == nullptr)))
       return set_error(RM_E_INVAL, "a rotation needs freqs and positions");
   }
   rm_kv_cache c = {};
   if (cache != nullptr) {
     RM_CHECK(check_cache(*cache, false));
     c = *cache;
-    if (slots == nullptr) return set_error(RM_E_INVAL, "a cache write needs slots");
+    if (T > 0 && slots == nullptr) return set_error(RM_E_INVAL, "a cache write needs slots");
     if (c.n_kv_heads != n_kv_heads || c.head_dim != head_dim)
       return set_error(RM_E_INVAL, "the cache has other heads");
   }
@@ -191,7 +191,7 @@ int rm_op_attn_window(const void* q, int64_t q_stride, const void* k, int64_t k_
                       const void* v, int64_t v_stride, const int32_t* offsets, int32_t n_seqs,
                       int32_t T, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                       int32_t window, int32_t sinks, void* out, int64_t out_stride, void* stream) {
-  if (q == nullptr || k == nullptr || v == nullptr || offsets == nullptr || out == nullptr)
+  if (offsets == nullptr || (T > 0 && (q == nullptr || k == nullptr || v == nullptr || out == nullptr)))
     return set_error(RM_E_INVAL, "NULL argument");
   if (n_seqs < 1 || T < 0 || !heads_ok(n_q_heads, n_kv_heads) || n_q_heads / n_kv_heads > 128 ||
       (head_dim != 64 && head_dim != 128) || window < 0 || sinks < 0)

@@ -372,7 +372,8 @@ int rm_op_kv_slots(const int32_t* len_before, const int32_t* n_new, int32_t n_se
  * not share a slot.  q_out and k_out may be the q and k columns of qkv itself
  * (in place); no other overlap.
  * head_dim a multiple of 8, 8..256; qkv, q_out, k_out 16-byte aligned with
- * strides that are multiples of 8 elements; T >= 0. */
+ * strides that are multiples of 8 elements.  T >= 0; T = 0 does nothing, and the
+ * buffers with an entry a token may be NULL then (those of an empty tensor). */
 int rm_op_qk_norm_rope(const void* qkv, int64_t qkv_stride, void* q_out, int64_t q_stride,
                        void* k_out, int64_t k_stride, int32_t T, int32_t n_q_heads,
                        int32_t n_kv_heads, int32_t head_dim, const float* q_gain,
@@ -392,7 +393,8 @@ int rm_op_qk_norm_rope(const void* qkv, int64_t qkv_stride, void* q_out, int64_t
  * them; a row whose seen scores are all -infinity is NaN.  Finite values are
  * taken up to |v| * keys = 2^87 (the sums of p v are divided at the end, and p
  * may reach 2^40 before its reference moves).  out overlaps no input.  head_dim 64 or 128; pointers 16-byte aligned, strides multiples of 8
- * elements; n_q_heads / n_kv_heads <= 128.  Waits that give up (none in normal
+ * elements; n_q_heads / n_kv_heads <= 128.  T >= 0; T = 0 does nothing, and q,
+ * k, v and out may be NULL then.  Waits that give up (none in normal
  * operation) are counted (rm_op_timeouts); the outputs are then invalid. */
 int rm_op_attn_window(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                       const void* v, int64_t v_stride, const int32_t* offsets, int32_t n_seqs,

@@ -142,6 +142,17 @@ def test_attn_window_refuses(kw):
     refused(lambda: rm.ops.attn_window(**{**WINDOW, **kw}))
 
 
+def test_steps_of_no_tokens_take_empty_buffers():
+    # an empty tensor has no address
+    rope = dict(qkv=None, q_out=None, k_out=None, T=0, positions=None, slots=None)
+    for more in ({}, dict(rope=None), dict(cache=None), dict(q_gain=None, k_gain=None)):
+        rm.ops.qk_norm_rope(**{**ROPE, "rope": rm.Rope(A, 64), "cache": cache(), **rope, **more})
+    rm.ops.attn_window(**{**WINDOW, "q": None, "k": None, "v": None, "out": None, "T": 0})
+    for kw in (dict(q_stride=64), dict(offsets_dev=None), dict(head_dim=32)):      # the rest is judged as ever
+        refused(lambda: rm.ops.attn_window(**{**WINDOW, "T": 0, **kw}))
+    refused(lambda: rm.ops.qk_norm_rope(**{**ROPE, **rope, "rope": rm.Rope(None, 64)}))
+
+
 DECODE = dict(q=A, q_stride=128, block_table=A, table_stride=4, length=A, n_seqs=3, n_q_heads=2, window=0, sinks=0, out=A,
               out_stride=128, workspace=A, workspace_bytes=1 << 30)
 

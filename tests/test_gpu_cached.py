@@ -273,6 +273,19 @@ def test_qk_norm_rope_without_cache_or_keys():
     torch.cuda.synchronize()
 
 
+def test_steps_of_no_tokens():
+    none = {d: torch.empty(0, dtype=d, device="cuda") for d in (torch.bfloat16, torch.int32, torch.int64)}
+    x, i32 = none[torch.bfloat16], none[torch.int32]
+    pool = torch.zeros(2, 4 * 16 * 64, dtype=torch.bfloat16, device="cuda")
+    cache = rm.KvCache(pool[0], pool[1], n_pages=4, page_size=16, n_kv_heads=1, head_dim=64)
+    rope = rm.Rope(dev(C.rope_freqs(64, 1e4), torch.float64), 64)
+    rm.ops.qk_norm_rope(x, 4 * 64, x, 128, x, 64, 0, 2, 1, 64, None, None, 0.0, rope, i32, cache, none[torch.int64])
+    rm.ops.attn_window(x, 128, x, 64, x, 64, dev([0, 0], torch.int32), 1, 0, 2, 1, 64, 0, 0, x, 128)
+    got = run_slots(np.array([5, 0]), np.array([0, 0]), np.arange(3), np.zeros((2, 1)), 0, 16, used=0)
+    torch.cuda.synchronize()
+    assert got[0].tolist() == [0, 0, 0] and got[3].tolist() == [5, 0] and got[4:6] == (0, 0) and (pool == 0).all()
+
+
 def test_qk_norm_rope_keeps_nan_and_saturates():
     T, d = 4, 64
     qkv = randn((T, 3 * d), 3)
