@@ -29,6 +29,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "paging.cuh"
 
 namespace rmk {
 namespace {
@@ -68,9 +69,8 @@ struct DecodeArgs {
   const void* kc;
   const void* vc;
   int64_t page_stride;
-  int n_pages, P;
-  uint32_t div;                 // x / P = x * div >> shift for 0 <= x < 2^31
-  int shift;
+  int n_pages;
+  PageDiv div;
   const float* k_scale;
   const float* v_scale;
   const int32_t* table;
@@ -91,7 +91,7 @@ struct Seen {
   int vis, nsink, skip, nt;
 };
 __device__ __forceinline__ Seen seen_of(const DecodeArgs& a, int s, int tile) {
-  const int64_t cap = static_cast<int64_t>(a.table_stride) * a.P;
+  const int64_t cap = static_cast<int64_t>(a.table_stride) * a.div.P;
   int len = max(0, a.length[s]);
   if (len > cap) len = static_cast<int>(cap);
   const int lo = a.window > 0 && len > a.window ? len - a.window : 0;
@@ -267,8 +267,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
     const unsigned j = static_cast<unsigned>(get.t) * SH::kTile + warp * kKeys + lane;
     if (lane < kKeys && j < static_cast<unsigned>(get.seen.vis)) {
       const int key = static_cast<int>(j) + (j < static_cast<unsigned>(get.seen.nsink) ? 0 : get.seen.skip);
-      const int b = static_cast<int>((static_cast<unsigned long long>(key) * a.div) >> a.shift);
-      row_in_page = static_cast<int64_t>(get.u / mtiles) * a.P + (key - b * a.P);
+      const int b = a.div.floor(key);
+      row_in_page = static_cast<int64_t>(get.u / mtiles) * a.div.P + (key - b * a.div.P);
       pg = a.table[static_cast<int64_t>(get.s) * a.table_stride + b];
     }
     get.next(a, SH::kTile);
@@ -667,7 +667,7 @@ cudaError_t launch(DecodeArgs a, int num_sms, cudaStream_t st) {
   const int group = a.hq / a.hkv;
   a.units = a.hkv * ((group + SH::kRows - 1) / SH::kRows);
   // no more CTAs than tiles of the longest possible contexts
-  const int64_t keys = static_cast<int64_t>(a.table_stride) * a.P;
+  const int64_t keys = static_cast<int64_t>(a.table_stride) * a.div.P;
   const int64_t most = static_cast<int64_t>(a.n) * a.units * ((keys + SH::kTile - 1) / SH::kTile + kUnitCost);
   const int grid = static_cast<int>(std::min<int64_t>(most, std::min(kMaxCtas, num_sms * kCtasPerSm)));
   auto kernel = attn_decode_kernel<D, E, NH>;
@@ -699,14 +699,7 @@ cudaError_t attn_decode_launch(const void* q, int64_t q_stride, const rm_kv_cach
   a.vc = c.v;
   a.page_stride = c.page_stride;
   a.n_pages = c.n_pages;
-  a.P = c.page_size;
-  // x / P for 0 <= x < 2^31 as x * ceil(2^shift / P) >> shift with 2^shift =
-  // 2^31 * (the power of two from P on): the multiplier fits 32 bits and
-  // exceeds 2^shift / P by less than 1, so the quotient is too large by less
-  // than 2^31 / 2^shift <= 1 / P
-  a.shift = 31;
-  while ((1 << (a.shift - 31)) < c.page_size) ++a.shift;
-  a.div = static_cast<uint32_t>(((1ull << a.shift) + c.page_size - 1) / c.page_size);
+  a.div = page_div(c.page_size);
   a.k_scale = c.k_scale;
   a.v_scale = c.v_scale;
   a.table = table;
