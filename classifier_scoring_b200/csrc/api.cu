@@ -1077,12 +1077,15 @@ int rm_build_checked(void) { return RMK_CHECKED; }
 
 int rm_bounds_errors(int64_t* out) {
   if (out == nullptr) return set_error(RM_E_INVAL, "NULL argument");
-  int32_t a = 0, b = 0, c = 0;
+  int64_t sum = 0;
   RM_CUDA(cudaDeviceSynchronize());
-  RM_CUDA(bounds_errors_rowops(&a, true));
-  RM_CUDA(bounds_errors_attention(&b, true));
-  RM_CUDA(bounds_errors_attention_tc(&c, true));
-  *out = static_cast<int64_t>(a) + b + c;
+  for (auto read : {bounds_errors_rowops, bounds_errors_attention, bounds_errors_attention_tc, bounds_errors_kvcache,
+                    bounds_errors_attention_decode, bounds_errors_attention_window}) {
+    int32_t n = 0;
+    RM_CUDA(read(&n, true));
+    sum += n;
+  }
+  *out = sum;
   return RM_OK;
 }
 

@@ -34,6 +34,8 @@
 namespace rmk {
 namespace {
 
+RMK_BOUNDS_UNIT(attention_decode)
+
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnitCost = 2;                    // a unit's beginning and end, in tiles
@@ -269,7 +271,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) attn_decode_kernel(const
       const int key = static_cast<int>(j) + (j < static_cast<unsigned>(get.seen.nsink) ? 0 : get.seen.skip);
       const int b = a.div.floor(key);
       row_in_page = static_cast<int64_t>(get.u / mtiles) * a.div.P + (key - b * a.div.P);
-      pg = a.table[static_cast<int64_t>(get.s) * a.table_stride + b];
+      if (in_bounds(get.s < a.n && b < a.table_stride && key - b * a.div.P >= 0 && key - b * a.div.P < a.div.P))
+        pg = a.table[static_cast<int64_t>(get.s) * a.table_stride + b];
     }
     get.next(a, SH::kTile);
   };
@@ -611,6 +614,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_decode_join_kernel(const De
   const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
   const int4 rec = a.parts.rec[c];
   if (rec.x < 0) return;
+  if (!in_bounds(rec.x < a.n && rec.y >= 0 && rec.y < a.units && rec.w >= c && rec.w < static_cast<int>(gridDim.x))) return;
   const int group = a.hq / a.hkv, mtiles = a.units / a.hkv;
   const int h = rec.y / mtiles, r0 = (rec.y % mtiles) * kRows;
   if (r0 + r >= group) return;
@@ -683,6 +687,15 @@ cudaError_t launch(DecodeArgs a, int num_sms, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t bounds_errors_attention_decode(int32_t* out, bool reset) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_bounds_attention_decode, sizeof(int32_t));
+  if (e == cudaSuccess && reset) {
+    const int32_t zero = 0;
+    e = cudaMemcpyToSymbol(g_bounds_attention_decode, &zero, sizeof(int32_t));
+  }
+  return e;
+}
 
 size_t attn_decode_workspace(int, int, const rm_kv_cache& c) {
   return static_cast<size_t>(kMaxCtas) * (2 * kMaxRows * (c.head_dim + 2) * sizeof(float) + sizeof(int4));

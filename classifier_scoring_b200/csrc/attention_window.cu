@@ -73,6 +73,8 @@
 namespace rmk {
 namespace {
 
+RMK_BOUNDS_UNIT(attention_window)
+
 __device__ int32_t g_window_err[ERR_WORDS];
 
 constexpr int kTile = 128;              // rows of a tile, keys of a chunk
@@ -428,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s0 = warp_upper_index(a.offsets, a.n, t0, lane);
           int o = a.offsets[s0], s = s0 + 1 + lane;
           const int start0 = max(0, min(t0, o));
+          if (lane == 0) in_bounds(o >= 0 && o <= t0);      // (offsets that begin behind 0 are cut to it)
           uint2* mine = reinterpret_cast<uint2*>(p.begins) + lane;     // eight tokens' bytes
           *mine = make_uint2(0u, 0u);
           __syncwarp();
@@ -865,6 +868,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int st = __shfl_sync(0xffffffffu, start, src), from = __shfl_sync(0xffffffffu, lo, src);
             const int se = __shfl_sync(0xffffffffu, sink_end, src);
             auto ptr = [&](int64_t j, const bf16*& kp, const bf16*& vp) {
+              if (!in_bounds(j >= 0 && j <= tt && tt < a.tmax)) return;
               kp = a.k + j * a.k_stride + h * D;
               vp = a.v + j * a.v_stride + h * D;
             };
@@ -918,6 +922,15 @@ cudaError_t launch(const WindowArgs& a, int T, int grid, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t bounds_errors_attention_window(int32_t* out, bool reset) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_bounds_attention_window, sizeof(int32_t));
+  if (e == cudaSuccess && reset) {
+    const int32_t zero = 0;
+    e = cudaMemcpyToSymbol(g_bounds_attention_window, &zero, sizeof(int32_t));
+  }
+  return e;
+}
 
 cudaError_t window_wait_selftest(unsigned long long limit_ns, cudaStream_t st) {
   window_wait_selftest_kernel<<<1, 32, 0, st>>>(limit_ns);

@@ -100,6 +100,9 @@ cudaError_t cvt_to_f32_launch(const void* src, int src_dtype, float* dst, size_t
 cudaError_t bounds_errors_rowops(int32_t* out, bool reset);
 cudaError_t bounds_errors_attention(int32_t* out, bool reset);
 cudaError_t bounds_errors_attention_tc(int32_t* out, bool reset);
+cudaError_t bounds_errors_kvcache(int32_t* out, bool reset);
+cudaError_t bounds_errors_attention_decode(int32_t* out, bool reset);
+cudaError_t bounds_errors_attention_window(int32_t* out, bool reset);
 
 // ---- attention (attention.cu) ----
 cudaError_t attn_scores_launch(const void* qkv, void* S, const int32_t* offsets,

@@ -13,6 +13,8 @@
 namespace rmk {
 namespace {
 
+RMK_BOUNDS_UNIT(kvcache)
+
 // ---------------------------------------------------------------------------
 // Slot maps.  Bound by latency: a few dependent reads, a scan and the writes
 // (2.9 us for a step of 64 requests, 5.7 us for 251k tokens of 1000, 3 MB).
@@ -137,8 +139,9 @@ __global__ void __launch_bounds__(1024, 1)
     *unserved = n - m;
   }
   for (int g = at; g < pages; g += all) {
-    const int i = upper_index(pg, m, g);
-    block_table[static_cast<int64_t>(i) * stride + div.ceil(before[i]) + (g - pg[i])] = free_pages[used + g];
+    const int i = upper_index(pg, m, g), b = div.ceil(before[i]) + (g - pg[i]);
+    if (!in_bounds(b >= 0 && b < stride && used + g < n_free)) continue;
+    block_table[static_cast<int64_t>(i) * stride + b] = free_pages[used + g];
   }
   // kRun consecutive tokens a thread: one search for their request, one
   // page lookup per page, wide stores
@@ -169,8 +172,9 @@ __global__ void __launch_bounds__(1024, 1)
       }
       if (look) {
         const int have = div.ceil(before[i]);
-        page = b < have ? block_table[static_cast<int64_t>(i) * stride + b]
-                        : free_pages[used + pg[i] + b - have];
+        if (in_bounds(i < m && b >= 0 && (b < have ? b < stride : used + pg[i] + b - have < n_free)))
+          page = b < have ? block_table[static_cast<int64_t>(i) * stride + b]
+                          : free_pages[used + pg[i] + b - have];
       }
       slot[k] = static_cast<int64_t>(page) * P + rem;
       pos[k] = p;
@@ -329,7 +333,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, RopeShape<LP>::kBlocks) qk_no
     const int64_t slot = RopeShape<LP>::kSlotFirst ? early : a.slots[t];
     if (slot >= 0 && slot < a.n_slots) {
       const int64_t page = slot <= 0x7fffffff ? a.div.floor(static_cast<int>(slot)) : slot / a.div.P;
-      cache_row = page * a.page_stride + (slot - page * a.div.P) * a.d;
+      if (in_bounds(slot - page * a.div.P >= 0 && slot - page * a.div.P < a.div.P))
+        cache_row = page * a.page_stride + (slot - page * a.div.P) * a.d;
     }
   }
   // the partner dims of an 8-dim chunk under RM_ROPE_HALF
@@ -513,6 +518,15 @@ cudaError_t slots_go(const int32_t* len_before, const int32_t* n_new, int n, int
 }
 
 }  // namespace
+
+cudaError_t bounds_errors_kvcache(int32_t* out, bool reset) {
+  cudaError_t e = cudaMemcpyFromSymbol(out, g_bounds_kvcache, sizeof(int32_t));
+  if (e == cudaSuccess && reset) {
+    const int32_t zero = 0;
+    e = cudaMemcpyToSymbol(g_bounds_kvcache, &zero, sizeof(int32_t));
+  }
+  return e;
+}
 
 cudaError_t kv_slots_launch(const int32_t* len_before, const int32_t* n_new, int n, int page_size,
                             const int32_t* free_pages, int n_free, const int32_t* used_before,

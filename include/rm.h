@@ -242,7 +242,8 @@ int rm_debug_fail_alloc(int32_t k);
  * the same library compiled with RM_CHECKED, in which the kernels test the
  * indices they derive from offsets and other per-call metadata (positions in
  * the position table, sequence and row-block indices, a tile's offsets
- * window, the softmax's row index) before the accesses those indices address,
+ * window, the softmax's row index, a paged cache's table, free-list and slot
+ * entries) before the accesses those indices address,
  * and skip the access and count it when a test fails (no trap, no assert).
  * rm_build_checked() returns 1 in that library and 0 in the product one.
  * rm_bounds_errors: waits for the device, writes the number of failed tests

@@ -806,7 +806,7 @@ def test_a_wait_that_gives_up_is_counted_and_told_once():
 @pytest.fixture(scope="module", autouse=True)
 def no_wait_gives_up(cuda):
     yield
-    assert rm.op_timeouts() == 0
+    assert rm.op_timeouts() == 0 and rm.bounds_errors() == 0      # (the second counts in the checked build alone)
 
 
 # --- what the device check refuses ---------------------------------------------------------

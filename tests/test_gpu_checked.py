@@ -53,6 +53,15 @@ def test_checked_build_counts_inconsistent_metadata_and_stays_usable():
     assert res["tiny_err_0"] <= SCORE_ATOL and res["tiny_err_1"] <= SCORE_ATOL
 
 
+def test_checked_build_of_incremental_scoring_with_no_failed_bound():
+    """The incremental-scoring kernels' own tests, in the checked library: the
+    same results, and at their end no failed bounds test and no wait given up."""
+    env = dict(os.environ, RMSCORE_LIB=rm.CHECKED_LIB_PATH, PYTHONPATH=ROOT)
+    r = subprocess.run([sys.executable, "-m", "pytest", "tests/test_gpu_cached.py", "-q", "-x", "-m", "gpu", "-p", "no:cacheprovider"],
+                       cwd=ROOT, env=env, capture_output=True, text=True, timeout=900)
+    assert r.returncode == 0 and " passed" in r.stdout, r.stdout[-2000:]
+
+
 def test_product_build_reports_no_checks():
     assert not rm.build_checked()
     assert rm.bounds_errors() == 0
