@@ -82,7 +82,10 @@ constexpr int kSoftmaxWarps = 16;
 constexpr int kThreads = 32 * (kSoftmaxWarps + 4);     // two MMA warps, TMA, planner
 constexpr float kLate = 40.f;           // log2; see the softmax
 constexpr int kPlans = 2;               // items planned ahead
-constexpr unsigned long long kLimitNs = 10000000000ull;
+// Limit of a wait: 10 s, and 50 us for each packed token of the call.  A tile's
+// roles wait while its softmax warps compute rows again (below): 32 rows a warp
+// at most, each over at most every token, 0.5 us a key measured.
+constexpr unsigned long long kLimitNs = 10000000000ull, kLimitNsPerToken = 50000ull;
 
 // A work item: kv head; first token and token counts of its tiles; start of
 // the sequence of a tile's first token, and that token's first key inside its
@@ -120,6 +123,7 @@ struct WindowArgs {
   int n, hq, hkv, group, tq, tmax, window, sinks, items;
   bf16* out;
   float scale_log2;
+  unsigned long long limit_ns;
 };
 
 // The issuing roles run as whole warps, whose control flow and operands stay
@@ -189,15 +193,10 @@ __device__ __forceinline__ int warp_upper_index(const int32_t* a, int n, int key
   return lo;
 }
 
-__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, unsigned long long limit_ns = kLimitNs) {
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, unsigned long long limit_ns) {
   if (mbar_wait_for(bar, parity, limit_ns)) return true;
   atomicAdd(&g_window_err[ERR_TIMEOUT], 1);
   return false;
-}
-
-// the same for a whole warp: all lanes leave with one answer
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, wait(bar, parity));
 }
 
 // Named barriers of the softmax: the 64 threads that share 32 rows of a tile
@@ -311,6 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   pdl_wait();
+  // a wait of a whole warp: all lanes leave with one answer
+  auto wait_warp = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity, a.limit_ns)) != 0; };
   const uint32_t tmem = *tmem_slot;
   auto s_at = [&](int x) { return tmem + static_cast<uint32_t>(x * kTile); };
   auto o_at = [&](int x) { return tmem + static_cast<uint32_t>(2 * kTile + x * kTile); };
@@ -970,6 +971,7 @@ cudaError_t attn_window_launch(const void* q, int64_t q_stride, const void* k, i
   a.sinks = sinks;
   a.out = static_cast<bf16*>(out);
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(d));
+  a.limit_ns = kLimitNs + kLimitNsPerToken * static_cast<unsigned long long>(T);
   const int64_t items = (static_cast<int64_t>(T) + 2 * a.tq - 1) / (2 * a.tq) * hkv;
   if (items > 0x7fffffff) return cudaErrorInvalidValue;
   a.items = static_cast<int>(items);

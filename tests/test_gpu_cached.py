@@ -484,6 +484,21 @@ def test_attn_window_scores_that_climb():
     assert np.all(np.abs(f64(out).reshape(T, 1, d) - ref) <= attention_bound(ref, mag, top))
 
 
+def test_attn_window_rows_computed_again_keep_nobody_waiting_too_long():
+    # every row but a chunk's first is computed again, by one warp: the tile's other roles wait, and no wait gives up
+    T, hq, hkv, d = 3000, 8, 2, 128
+    q = torch.ones(T, hq * d, dtype=torch.bfloat16, device="cuda")
+    k = (torch.arange(T, device="cuda")[:, None] * torch.ones(hkv * d, device="cuda") * 0.1).to(torch.bfloat16)
+    v = randn((T, hkv * d), 3)
+    out = torch.empty_like(q)
+    rm.ops.attn_window(q, hq * d, k, hkv * d, v, hkv * d, dev([0, T], torch.int32), 1, T, hq, hkv, d, 0, 0, out, hq * d)
+    torch.cuda.synchronize()
+    assert rm.op_timeouts() == 0
+    x = [t.view(T, h, d) for t, h in ((q, hq), (k, hkv), (v, hkv))]
+    ref, mag, top = window_on_device(*x, [0, T], 0, 0)
+    assert np.all(np.abs(f64(out).reshape(T, hq, d) - ref) <= attention_bound(ref, mag, top))
+
+
 def test_attention_of_large_values():
     # values near the documented bounds, the window's under scores that climb
     T, d = 700, 128
