@@ -7,8 +7,8 @@
 //  - the (sequence, kv head) units' key tiles, laid end to end, are cut into
 //    one equal stretch per CTA whatever the lengths are, so a long context
 //    beside short ones does not leave SMs idle and no length needs to be known
-//    on the host.  A unit that a cut divides leaves its parts (running maximum,
-//    sum, unnormalised output) in the workspace; a second kernel joins them in
+//    on the host.  A unit that a cut divides leaves its parts (reference, sum,
+//    unnormalised output) in the workspace; a second kernel joins them in
 //    stretch order.
 //  - each warp of a CTA takes its own keys of every tile through a private
 //    ring of cp.async stages, with no barrier between warps until a unit ends;
@@ -17,11 +17,13 @@
 //    (m16n8k16: 16 keys by 8 heads for the scores, 16 dims by 8 heads for the
 //    output), so a key is read once for all of them and a step's arithmetic
 //    follows the head count, eight at a time.
-// Measured on B200: 24 contexts of up to 131071 tokens, 32 heads on 8 of 128
-// dims: 188 us, 6.4 TB/s (98% of a copy's rate); 64 contexts of 256 to 560
-// tokens, 16 heads of 128: 41 us, 5.2 TB/s (the rings' ramp and two launches);
-// 128 windows over e4m3 pages: 86 us, 5.9 TB/s (the conversions take 45% of
-// the issue slots); one context of 500 tokens: 6.7 us, latency.
+// Measured on B200, among calls on other inputs (in brackets: replayed on the
+// same ones): 24 contexts of up to 131071 tokens, 32 heads on 8 of 128 dims:
+// 193 us (192), 6.3 TB/s (95% of a copy's rate); 64 contexts of 256 to 560
+// tokens, 16 heads of 128: 42 us (42), 5.1 TB/s (the rings' ramp and two
+// launches); 128 windows over e4m3 pages: 94 us (86), 5.4 TB/s (the conversions
+// take 45% of the issue slots); one context of 500 tokens: 9.4 us (6.8),
+// latency.
 #include <cuda_fp8.h>
 
 #include <algorithm>

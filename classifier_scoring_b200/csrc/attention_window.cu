@@ -56,12 +56,15 @@
 // Every wait is bounded; one that gives up counts into the error word that
 // rm_op_timeouts reads, and its role stops.
 //
-// Measured on B200: five documents of up to 32761 tokens, 32 heads on 8 of 128
-// dims, window 4096: 2.05 ms, 1.0 PFLOP/s of seen pairs (bound by a chunk's
+// Measured on B200, among calls on other inputs (in brackets: replayed on the
+// same ones): five documents of up to 32761 tokens, 32 heads on 8 of 128 dims,
+// window 4096: 2.10 ms (2.03), 1.0 PFLOP/s of seen pairs (bound by a chunk's
 // chain of scores, softmax and products with two tiles in flight, and by the
-// power cap); 64 prompts of 256 to 560 tokens, 16 heads of 128: 139 us (an
+// power cap); 64 prompts of 256 to 560 tokens, 16 heads of 128: 155 us (140; an
 // item is 1 to 5 chunks long, so its first maximum and its end weigh); 64
-// texts of 2 to 100 tokens, 12 heads of 64: 16 us (latency).
+// texts of 2 to 100 tokens, 12 heads of 64: 16 us (latency).  Where every row
+// is computed again (one document of 4096 tokens, 16 heads of 128, scores that
+// climb): 59 ms instead of 97 us.
 #include <cuda.h>
 
 #include <algorithm>

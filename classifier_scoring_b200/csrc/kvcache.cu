@@ -17,15 +17,16 @@ RMK_BOUNDS_UNIT(kvcache)
 
 // ---------------------------------------------------------------------------
 // Slot maps.  Bound by latency: a few dependent reads, a scan and the writes
-// (2.9 us for a step of 64 requests, 5.7 us for 251k tokens of 1000, 3 MB).
+// (on the device 2.9 us for a step of 64 requests, 5.9 us for 251k tokens of
+// 1000, 3 MB; a call among others 8 us, the host's time).
 // Every CTA scans the n requests for itself (n is small beside the tokens, and
 // a scan costs less than handing its result on through memory), then the
 // tokens and new pages are shared out over all threads.  len_after and
 // used_after may be len_before and used_before: then all CTAs form one cluster
-// whose barrier separates the reads from the writes.
+// whose barrier separates the reads from the writes (24 us for the 251k tokens).
 // ---------------------------------------------------------------------------
 // Tokens a thread takes in a row: eight share a search, a page lookup and wide
-// stores (251k tokens of 1000 requests: 5.7 us); one where every thread has at
+// stores (251k tokens of 1000 requests: 5.9 us); one where every thread has at
 // most one, whose lookups then do not wait for one another.
 constexpr int kSlotRun = 8;
 constexpr int kSlotSingles = 148 * 256;
@@ -212,8 +213,9 @@ __global__ void __launch_bounds__(1024, 1)
 // warps meet, and a head is read whole before it is written, so the outputs
 // may lie over the input.
 // Measured on B200, 25k tokens of 16 + 16 + 16 heads of 128, normed and
-// rotated into a bf16 cache: 138 us, 5.3 TB/s, 80% of a copy's rate (partners
-// through shared memory: 3 us more).
+// rotated into a bf16 cache: 142-144 us among calls on other inputs, 5.1 TB/s,
+// 78% of a copy's rate (138-141 replayed on the same ones; partners through
+// shared memory: 3 us more).
 // ---------------------------------------------------------------------------
 constexpr int kRopeWarps = 4;
 constexpr int kRopeMaxDim = 256;
@@ -491,8 +493,8 @@ cudaError_t slots_go(const int32_t* len_before, const int32_t* n_new, int n, int
   }
   const PageDiv div = page_div(page_size);
   // One CTA for a step's few tokens; a run of tokens per thread over many CTAs
-  // for prompts (251k tokens of 1000 requests: 25.8 us on one cluster of eight
-  // CTAs); one cluster when the lengths advance in place.
+  // for prompts (251k tokens of 1000 requests: 24 us on one cluster of eight
+  // CTAs, 5.9 us on 123); one cluster when the lengths advance in place.
   const int64_t runs = (static_cast<int64_t>(T) + kRun - 1) / kRun;
   const bool in_place = len_after == len_before || used_after == used_before;
   const int threads = n > kSlotStaged ? 1024 : 256;

@@ -1,8 +1,10 @@
 /*
  * rm_ops.h -- one C entry point per step of the scoring hot path.
  *
- * rm_score (rm.h) chains exactly these launchers; they are exported so that
- * each step can be checked on its own against the fp64 oracle.  All pointers
+ * The launchers that rm_score (rm.h) chains are exported here, so that each
+ * step can be checked on its own against the fp64 oracle; beside them stand
+ * steps that rm_score never takes (the vote, the attention without an
+ * allocation, the steps of incremental scoring).  All pointers
  * are DEVICE pointers unless marked host; all work is asynchronous on stream
  * (a cudaStream_t as void*).  Return RM_OK or a negative RM_E_* code (rm.h);
  * arguments are validated on the host before anything is enqueued.
@@ -266,8 +268,9 @@ int rm_op_attention_noalloc(const void* qkv, void* ctx, const int32_t* offsets, 
  * Unlike the steps above, these take grouped heads (n_q_heads a multiple of
  * n_kv_heads; query head j reads key-value head j / (n_q_heads / n_kv_heads))
  * and rows with a pitch (row_stride elements from one token to the next).
- * Every device pointer must belong to the current CUDA device; an output
- * pointer that does not (host memory, or another device's) gives RM_E_INVAL.
+ * Every device pointer must belong to the current CUDA device.  One a call
+ * (offsets of rm_op_kv_slots, q_out, out) is looked up: host memory or another
+ * device's gives RM_E_INVAL; the others are taken on trust.
  * None of them allocates or keeps anything between calls; all can be captured
  * in a CUDA graph.
  * ------------------------------------------------------------------------- */
@@ -363,14 +366,18 @@ int rm_op_kv_slots(const int32_t* len_before, const int32_t* n_new, int32_t n_se
  *                                              4-byte aligned; both NULL =
  *                                              no norm)
  *   z = y with its first rot_dim dims rotated by positions[t] (rope NULL: z = y)
- * in fp32, angles reduced in 64 bits (exact to fp32 rounding for any int32
- * position), rounded once.  Written: q_out (row t's query heads), k_out (its
- * key heads; NULL = not written), and, when cache != NULL, the key and value
- * heads to slots[t] of the cache (bf16, or x / scale rounded to the nearest
- * 8-bit value, +-448 at most, NaN kept).  A token whose slot is negative or
- * beyond the cache's last page is not written to the cache.  Two tokens must
- * not share a slot.  q_out and k_out may be the q and k columns of qkv itself
- * (in place); no other overlap.
+ * in fp32, rounded once.  The squares of a head must add up to less than 2^128;
+ * a head of zeros with eps = 0 is NaN.  The angle position * freqs[i] is
+ * computed and freed of whole turns in 64 bits: it is off by at most 3 * 2^-53
+ * of itself (with freqs[i] <= 1 less than 2^-24 radians up to position 2^27,
+ * 7e-7 at 2^31), and then rounded to fp32.
+ * Written: q_out (row t's query heads), k_out (its key heads; NULL = not
+ * written), and, when cache != NULL, the key and value heads to slots[t] of the
+ * cache (bf16, or x * (1 / scale), both in fp32, rounded to the nearest 8-bit
+ * value, +-448 at most, NaN kept).  A token whose slot is negative or beyond
+ * the cache's last page is not written to the cache.  Two tokens must not share
+ * a slot.  q_out and k_out may be the q and k columns of qkv itself (in place);
+ * no other overlap.
  * head_dim a multiple of 8, 8..256; qkv, q_out, k_out 16-byte aligned with
  * strides that are multiples of 8 elements.  T >= 0; T = 0 does nothing, and the
  * buffers with an entry a token may be NULL then (those of an empty tensor). */
@@ -390,12 +397,16 @@ int rm_op_qk_norm_rope(const void* qkv, int64_t qkv_stride, void* q_out, int64_t
  * int32[n_seqs+1], offsets[0] = 0, non-decreasing (empty sequences allowed),
  * offsets[n_seqs] <= T (cut to it); rows behind it are not written.  Values
  * and keys that a row does not see do not reach it, infinities and NaN among
- * them; a row whose seen scores are all -infinity is NaN.  Finite values are
- * taken up to |v| * keys = 2^87 (the sums of p v are divided at the end, and p
- * may reach 2^40 before its reference moves).  out overlaps no input.  head_dim 64 or 128; pointers 16-byte aligned, strides multiples of 8
- * elements; n_q_heads / n_kv_heads <= 128.  T >= 0; T = 0 does nothing, and q,
- * k, v and out may be NULL then.  Waits that give up (none in normal
- * operation) are counted (rm_op_timeouts); the outputs are then invalid. */
+ * them; a row whose seen scores are all -infinity is NaN.  Rows that an unseen
+ * infinity or NaN would have reached, and rows whose weights rise by more than
+ * 2^40 from one stretch of 128 keys to the next, are computed again by a warp
+ * each: exact, but at about 0.5 us a key.  Finite values are taken up to
+ * |v| * keys = 2^87 (the sums of p v are divided at the end, and p may reach
+ * 2^40 before its reference moves).  out overlaps no input.  head_dim 64 or
+ * 128; pointers 16-byte aligned, strides multiples of 8 elements;
+ * n_q_heads / n_kv_heads <= 128.  T >= 0; T = 0 does nothing, and q, k, v and
+ * out may be NULL then.  Waits that give up (none in normal operation) are
+ * counted (rm_op_timeouts); the outputs are then invalid. */
 int rm_op_attn_window(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                       const void* v, int64_t v_stride, const int32_t* offsets, int32_t n_seqs,
                       int32_t T, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
