@@ -966,6 +966,62 @@ def test_prompts_then_steps_like_the_whole_texts(window, sinks, kind, graph):
             assert np.all(np.abs(f64(o[i]).reshape(hq, d) - ref) <= attention_bound(ref, mag, top)), (j, i)
 
 
+@pytest.mark.parametrize("graph", [False, True])
+def test_two_batches_at_once_on_streams_of_their_own(graph):
+    """Prompts and steps of two batches interleaved on two streams (eagerly, or
+    as two captured steps replayed at once) give what each gives alone."""
+    n, hidden, steps = 70, 64, 12
+    lens = np.random.RandomState(3).randint(1, 200, n)
+    kinds = (("bf16", 0, 0), ("e4m3", 50, 3))
+
+    def batch(which):
+        kind, window, sinks = kinds[which]
+        return Stepper(n, 8, 2, 128, 16, 1200, 16, window, sinks, kind, hidden, 40 + which)
+
+    xs = [[randn((int(lens.sum()), hidden), 50 + w)] + [randn((n, hidden), 60 + 20 * w + i) for i in range(steps)] for w in range(2)]
+    new = dev(lens, torch.int32)
+
+    def go(S, w, streams):
+        b, x = S.buffers(n), torch.empty(n, hidden, dtype=torch.bfloat16, device="cuda")
+        b["qkv"] = torch.empty(n, 12 * 128, dtype=torch.bfloat16, device="cuda")
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph() if graph else None
+        if graph:
+            x.copy_(xs[w][1])
+            torch.cuda.synchronize()
+            with torch.cuda.graph(g, stream=streams[w]):
+                S.step(x, b, stream=streams[w])
+        with torch.cuda.stream(streams[w]):
+            p = S.buffers(xs[w][0].shape[0])
+            y = S.prepare(xs[w][0], new, p, stream=streams[w])
+            rm.ops.attn_window(p["q"], 1024, p["k"], 256, y[:, 10 * 128:], y.shape[1], S.offsets, n, y.shape[0], 8, 2, 128, S.window,
+                               S.sinks, p["out"], 1024, stream=streams[w])
+            outs = [p["out"]]
+        for i in range(steps):
+            with torch.cuda.stream(streams[w]):
+                x.copy_(xs[w][1 + i])
+                if graph:
+                    g.replay()
+                else:
+                    S.step(x, b, stream=streams[w])
+                outs.append(b["out"].clone())
+            yield None
+        yield outs + [S.length, S.used, S.table, *S.pools, y, x, g]
+
+    alone = []
+    for w in range(2):
+        alone.append([o for o in go(batch(w), w, [torch.cuda.Stream(), torch.cuda.Stream()])][-1])
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    runs = [go(batch(w), w, streams) for w in range(2)]
+    both = [None, None]
+    for _ in range(steps + 1):
+        both = [next(r) for r in runs]
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        assert all(torch.equal(s.view(torch.uint8), t.view(torch.uint8)) for s, t in zip(a[:-1], b[:-1]))
+
+
 def test_a_prompt_scored_whole_and_token_by_token_agree():
     """The window attention over a text and the decode attention of each of
     its tokens in turn round alike up to their tolerances."""
